@@ -19,7 +19,8 @@
  *   - Every device pointer must be 16-byte aligned; d_model % 8 == 0; for the
  *     column-major layout also d_ff % 8 == 0.  Violations return
  *     DFK_ERR_MISALIGNED / DFK_ERR_UNSUPPORTED_SHAPE without launching.
- *   - 0 <= B <= 64 (decode batch).  B == 0 is a no-op returning DFK_OK.
+ *   - 0 <= B <= 64 (decode batch; the block-scaled FP8 operators take any
+ *     number of tokens M).  B == 0 is a no-op returning DFK_OK.
  *   - `stream` is a cudaStream_t (NULL = the legacy default stream).  Calls
  *     are asynchronous: the return code covers argument validation and
  *     launch errors only; a device-side failure (a pipeline wait that gave
@@ -249,6 +250,63 @@ DFK_API int dfk_rmsnorm_qkv_proj(const void *x, const void *gamma, float eps,
                                  const void *w_qkv, void *q, void *k, void *v, int B,
                                  int d_model, int n_q, int n_k, int n_v, int variant,
                                  void *stream);
+
+/* ---- block-scaled FP8 -------------------------------------------------------
+ * The MLP with both operands in 8 bits (GPULlama3.java PR #78 keeps the
+ * dequantisation inside the product; here the activations are 8-bit too), at
+ * any number of tokens: one decoded token up to a whole prompt.
+ *
+ * Activations [M][K]: E4M3 codes q and one fp32 scale per token and group of
+ * 128 along K, stored group by group, s[G][M] with G = ceil(K / 128):
+ *   a = max |v| over the group (the last may be shorter),
+ *   s = max(a / 448, 2^-126),  q = E4M3(v / s), round to nearest even.
+ * A NaN in a group makes its scale and all its codes NaN; an infinity makes
+ * the scale infinite, its own code NaN and the finite elements' codes 0: the
+ * token's products are NaN, other tokens are untouched.
+ * Weights [N][K]: E4M3 codes, row-major, and one fp32 scale per block of
+ * 128 x 128, s[ceil(N / 128)][G].
+ *
+ * Shared rules: 0 <= M (no upper limit of 64 here; M == 0 is a no-op
+ * returning DFK_OK); K, and the row length of a quantised output, a multiple
+ * of 16; any N otherwise.  Codes, bf16 tensors: 16-byte aligned; scales: 4-byte
+ * aligned.  Sums are fp32: exact products of codes, summed per group by
+ * the tensor core, scaled by s_x s_w and added in fp32 in a fixed order (the
+ * same bits on every call).  No workspace and no allocation: calls may run on
+ * several streams at once and be captured in graphs.  Inputs and outputs must
+ * not overlap, except residual_out with x or residual (the same pointer).
+ * Weights, their scales and gamma are read before the previous kernel in
+ * the stream has finished, as above.
+ */
+
+/* q, s = the codes and scales of x [M][K] bf16. */
+DFK_API int dfk_quant_fp8_block(const void *x, void *q, float *s, int M, int K, void *stream);
+
+/*
+ * The residual's addition, the RMSNorm and the quantisation in one pass:
+ *   r = bf16(x + residual), stored to residual_out
+ *   v = (r / sqrt(mean_k r^2 + eps)) * gamma  in fp32, not rounded to bf16
+ *   q, s = the codes and scales of v
+ *   x, residual, residual_out  [M][d_model] bf16; residual == NULL (with
+ *   residual_out == NULL): r = x, nothing stored.  d_model <= 32768.
+ */
+DFK_API int dfk_add_rmsnorm_fp8_block(const void *x, const void *residual, const void *gamma,
+                                      float eps, void *residual_out, void *q, float *s, int M,
+                                      int d_model, void *stream);
+
+/* y[m][n] = bf16( sum_k (s_x q_x)[m][k] (s_w q_w)[n][k] ): a down, QKV or output projection. */
+DFK_API int dfk_gemm_fp8_block(const void *q_x, const float *s_x, const void *q_w,
+                               const float *s_w, void *y, int M, int K, int N, void *stream);
+
+/*
+ * h = SiLU(x . W_gate^T) (*) (x . W_up^T), both projections, the activation
+ * and the product in one kernel.  Either h [M][d_ff] bf16 (q_h, s_h NULL), or
+ * h == NULL and q_h [M][d_ff], s_h [ceil(d_ff / 128)][M]: h quantised from its
+ * fp32 values, the input of the down projection.
+ */
+DFK_API int dfk_swiglu_gate_up_fp8_block(const void *q_x, const float *s_x, const void *q_gate,
+                                         const float *s_gate, const void *q_up,
+                                         const float *s_up, void *h, void *q_h, float *s_h,
+                                         int M, int d_model, int d_ff, void *stream);
 
 /*
  * Profiler-driven variant choice ("Deep Kernel Fusion for Transformer

@@ -69,6 +69,8 @@ EXPORTED = (
     "dfk_tp_group_create", "dfk_tp_group_connect", "dfk_tp_down_proj_allreduce",
     "dfk_tp_group_destroy", "dfk_tp_down_proj_allreduce_emulated",
     "dfk_mlp_stack_workspace_bytes", "dfk_mlp_stack_step",
+    "dfk_quant_fp8_block", "dfk_add_rmsnorm_fp8_block", "dfk_gemm_fp8_block",
+    "dfk_swiglu_gate_up_fp8_block",
 )
 
 
@@ -139,6 +141,10 @@ def lib():
                 "dfk_tp_group_destroy": [vp],
                 "dfk_tp_down_proj_allreduce_emulated": [i, vp, vp, vp, i, i, i, vp],
                 "dfk_mlp_stack_step": [vp, f, vp, vp, i, vp, vp, vp, vp, vp, ll, i, i, i, i, vp],
+                "dfk_quant_fp8_block": [vp, vp, vp, i, i, vp],
+                "dfk_add_rmsnorm_fp8_block": [vp, vp, vp, f, vp, vp, vp, i, i, vp],
+                "dfk_gemm_fp8_block": [vp, vp, vp, vp, vp, i, i, i, vp],
+                "dfk_swiglu_gate_up_fp8_block": [vp, vp, vp, vp, vp, vp, vp, vp, vp, i, i, i, vp],
                 "dfk_status_string": [i],
                 "dfk_last_error": [],
                 "dfk_version": [],
@@ -349,6 +355,137 @@ def dfk_rmsnorm_qkv_proj(x, gamma, eps, w_qkv, n_q, n_k, n_v, q=None, k=None, v=
                                       _ptr(outs[2]) if n_v else None,
                                       B, D, n_q, n_k, n_v, int(variant), _stream(stream)))
     return tuple(outs)
+
+
+# ---- block-scaled FP8: any number of tokens, 8-bit activations
+
+_FP8_CODES = (torch.float8_e4m3fn, torch.uint8)
+
+
+def _fb_check(name, t, dtypes, shape, device):
+    if not (isinstance(t, torch.Tensor) and t.is_cuda and t.dtype in dtypes):
+        raise DfkError(DFK_ERR_INVALID_ARG, "%s must be a CUDA tensor of %s"
+                       % (name, " or ".join(str(d)[6:] for d in dtypes)))
+    if tuple(t.shape) != shape or not t.is_contiguous():
+        raise DfkError(DFK_ERR_INVALID_ARG, "%s must be contiguous, of shape %s" % (name, shape))
+    if t.device != device:
+        raise DfkError(DFK_ERR_INVALID_ARG, "%s is on %s, not on %s" % (name, t.device, device))
+
+
+def _fb_rows(name, t):
+    """The [M, K] tensor that the other arguments' sizes and device go by."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dim() != 2:
+        raise DfkError(DFK_ERR_INVALID_ARG, "%s must be a 2-D CUDA tensor" % name)
+    return t.shape[0], t.shape[1], t.device
+
+
+def _fb_call(device, stream, fn, *args):
+    """fn(*args, stream) with `device` current: the call's own stream is the given one, or the
+    current one of that device."""
+    if device.index == torch.cuda.current_device():
+        _check(fn(*args, _stream(stream)))
+    else:
+        with torch.cuda.device(device):
+            _check(fn(*args, _stream(stream)))
+
+
+def _fb_out(shape, dtype, device, stream):
+    """An output the caller did not give, allocated for the stream that writes it."""
+    t = torch.empty(shape, dtype=dtype, device=device)
+    if stream is not None and t.numel():
+        t.record_stream(stream if hasattr(stream, "cuda_stream")
+                        else torch.cuda.ExternalStream(int(stream), device=device))
+    return t
+
+
+def _fb_codes_out(q, s, M, K, device, stream):
+    if q is None:
+        q = _fb_out((M, K), torch.float8_e4m3fn, device, stream)
+    else:
+        _fb_check("q", q, _FP8_CODES, (M, K), device)
+    if s is None:
+        s = _fb_out((-(-K // 128), M), torch.float32, device, stream)
+    else:
+        _fb_check("s", s, (torch.float32,), (-(-K // 128), M), device)
+    return q, s
+
+
+def dfk_quant_fp8_block(x, q=None, s=None, stream=None):
+    """Block-scaled FP8 of x [M, K] bf16: returns (q [M, K] float8_e4m3fn, s [ceil(K/128), M]
+    fp32), s = max(max|x| / 448, 2^-126) per token and group of 128, q = E4M3(x / s)."""
+    M, K, dev = _fb_rows("x", x)
+    _fb_check("x", x, (_BF16,), (M, K), dev)
+    q, s = _fb_codes_out(q, s, M, K, dev, stream)
+    _fb_call(dev, stream, lib().dfk_quant_fp8_block, _ptr(x), _ptr(q), _ptr(s), M, K)
+    return q, s
+
+
+def dfk_add_rmsnorm_fp8_block(x, residual, gamma, eps, residual_out=None, q=None, s=None,
+                              stream=None):
+    """r = bf16(x + residual) (r = x for residual None), then the block-scaled FP8 of
+    RMSNorm(r; gamma, eps): returns (q, s, r), r None without a residual.  residual_out may be
+    `residual` or `x` itself: the sum is then kept in place."""
+    M, D, dev = _fb_rows("x", x)
+    _fb_check("x", x, (_BF16,), (M, D), dev)
+    _fb_check("gamma", gamma, (_BF16,), (D,), dev)
+    if residual is not None:
+        _fb_check("residual", residual, (_BF16,), (M, D), dev)
+        if residual_out is None:
+            residual_out = _fb_out((M, D), _BF16, dev, stream)
+    if residual_out is not None:
+        _fb_check("residual_out", residual_out, (_BF16,), (M, D), dev)
+    q, s = _fb_codes_out(q, s, M, D, dev, stream)
+    _fb_call(dev, stream, lib().dfk_add_rmsnorm_fp8_block, _ptr(x), _ptr(residual), _ptr(gamma),
+             float(eps), _ptr(residual_out), _ptr(q), _ptr(s), M, D)
+    return q, s, residual_out
+
+
+def _fb_operands(q_x, s_x, weights):
+    M, K, dev = _fb_rows("q_x", q_x)
+    G = -(-K // 128)
+    _fb_check("q_x", q_x, _FP8_CODES, (M, K), dev)
+    _fb_check("s_x", s_x, (torch.float32,), (G, M), dev)
+    N = _fb_rows(*weights[0][:2])[0]
+    for name, q, s in weights:
+        _fb_check(name, q, _FP8_CODES, (N, K), dev)
+        _fb_check("s" + name[1:], s, (torch.float32,), (-(-N // 128), G), dev)
+    return M, K, N, dev
+
+
+def dfk_gemm_fp8_block(q_x, s_x, q_w, s_w, y=None, stream=None):
+    """y = x W^T, x in block-scaled FP8 (q_x [M, K], s_x [ceil(K/128), M]), W as E4M3 codes
+    q_w [N, K] with one fp32 scale per 128 x 128 block, s_w [ceil(N/128), ceil(K/128)];
+    returns y [M, N] bf16."""
+    M, K, N, dev = _fb_operands(q_x, s_x, (("q_w", q_w, s_w),))
+    if y is None:
+        y = _fb_out((M, N), _BF16, dev, stream)
+    else:
+        _fb_check("y", y, (_BF16,), (M, N), dev)
+    _fb_call(dev, stream, lib().dfk_gemm_fp8_block, _ptr(q_x), _ptr(s_x), _ptr(q_w), _ptr(s_w),
+             _ptr(y), M, K, N)
+    return y
+
+
+def dfk_swiglu_gate_up_fp8_block(q_x, s_x, q_gate, s_gate, q_up, s_up, fp8_out=True, h=None,
+                                 q_h=None, s_h=None, stream=None):
+    """h = SiLU(x W_gate^T) * (x W_up^T) in one kernel, operands as for dfk_gemm_fp8_block
+    (W_gate, W_up [d_ff, d_model]).  fp8_out: returns (q_h, s_h), h in block-scaled FP8 from its
+    fp32 values; otherwise returns h [M, d_ff] bf16."""
+    M, D, F, dev = _fb_operands(q_x, s_x, (("q_gate", q_gate, s_gate), ("q_up", q_up, s_up)))
+    if fp8_out:
+        if h is not None:
+            raise DfkError(DFK_ERR_INVALID_ARG, "h is the bf16 output: fp8_out=False")
+        q_h, s_h = _fb_codes_out(q_h, s_h, M, F, dev, stream)
+    else:
+        if q_h is not None or s_h is not None:
+            raise DfkError(DFK_ERR_INVALID_ARG, "q_h and s_h are the FP8 output: fp8_out=True")
+        if h is None:
+            h = _fb_out((M, F), _BF16, dev, stream)
+        else:
+            _fb_check("h", h, (_BF16,), (M, F), dev)
+    _fb_call(dev, stream, lib().dfk_swiglu_gate_up_fp8_block, _ptr(q_x), _ptr(s_x), _ptr(q_gate),
+             _ptr(s_gate), _ptr(q_up), _ptr(s_up), _ptr(h), _ptr(q_h), _ptr(s_h), M, D, F)
+    return (q_h, s_h) if fp8_out else h
 
 
 def dfk_gemv(x, w, out=None, variant=0, stream=None):

@@ -27,6 +27,7 @@
 #include <tuple>
 #include <vector>
 
+#include "api_internal.h"
 #include "cc_engine.cuh"
 #include "cc_key.h"
 #include "dfk.h"
@@ -940,6 +941,58 @@ int down_proj_with_scratch(const void *h, const void *w_down, void *y, int B, in
 }
 
 static bool misaligned(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) != 0; }
+
+// ---------------------------------------------------------------- api_internal.h
+
+int api_fail(int status, const char *fmt, ...) {
+  char buf[512];
+  va_list ap;
+  va_start(ap, fmt);
+  vsnprintf(buf, sizeof buf, fmt, ap);
+  va_end(ap);
+  t_last_error = buf;
+  return status;
+}
+
+int api_cuda_error(cudaError_t e, const char *what) {
+  cudaGetLastError();
+  return cuda_fail(e, what);
+}
+
+int api_device(int *sms, unsigned **err) {
+  DeviceState *ds;
+  const int rc = current_device(&ds);
+  if (rc) return rc;
+  *sms = ds->sms;
+  *err = ds->err;
+  return DFK_OK;
+}
+
+int api_tensor_map_u8(const void *ptr, uint64_t inner, uint64_t outer, uint64_t pitch,
+                      uint32_t box_inner, uint32_t box_outer, CUtensorMap *out) {
+  const int rc = get_encoder();
+  if (rc) return rc;
+  const cuuint64_t dims[2] = {inner, outer}, strides[1] = {pitch};
+  const cuuint32_t box[2] = {box_inner, box_outer}, ones[2] = {1, 1};
+  const CUresult r = g_encode(out, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void *>(ptr),
+                              dims, strides, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS)
+    return fail(DFK_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d), %llu x %llu bytes, box %u x %u",
+                static_cast<int>(r), static_cast<unsigned long long>(inner),
+                static_cast<unsigned long long>(outer), box_inner, box_outer);
+  return DFK_OK;
+}
+
+int api_allow_smem(const void *fn) {
+  int dev = 0;
+  const cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return api_cuda_error(e, "cudaGetDevice");
+  return ensure_smem_attr(dev, fn);
+}
+
+bool api_pdl() { return pdl_enabled(); }
 
 // ---------------------------------------------------------------- tensor parallel
 

@@ -1,0 +1,137 @@
+// fp8_block.cuh -- block-scaled FP8: the quantisation rule every kernel of
+// these operators shares, cluster helpers, and the launch interface.
+//
+// A vector v is stored in groups of 128 along its last dimension as E4M3
+// codes q and one fp32 scale s per group:
+//   a = max |v| over the group,  s = max(a / 448, 2^-126),  q = E4M3(v / s).
+// 448 is E4M3's largest value, so |v / s| <= 448 (1 + 2^-23), which rounds to
+// 448.  The floor 2^-126 (the smallest normal fp32) keeps s normal for tiny
+// groups and non-zero for an all-zero one (codes 0).  A NaN in the group makes
+// s and every code NaN; an infinity makes s infinite, its own code NaN and
+// the finite elements' codes 0.
+#pragma once
+#include <cuda.h>
+#include <cuda_runtime.h>
+#include <cstdint>
+
+#include "ptx.cuh"
+
+namespace dfk {
+
+constexpr int FB_GROUP = 128;
+constexpr float FB_E4M3_MAX = 448.f;
+
+// max that returns NaN when either operand is NaN (fmaxf drops it).
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+
+// A group's scale and the two factors of the quotient v / s.
+struct FbScale {
+  float s;    // the stored scale
+  float inv;  // 1 / s, rounded to nearest
+  float sr;   // s in the residual; 0 for an infinite s, where inv is 0 too
+};
+
+__device__ __forceinline__ FbScale fb_scale(float amax) {
+  FbScale f;
+  f.s = max_nan(amax / FB_E4M3_MAX, 1.17549435e-38f);
+  f.inv = 1.0f / f.s;
+  f.sr = f.s > 3.402823466e38f ? 0.f : f.s;
+  return f;
+}
+
+// v / s rounded to nearest, from the correctly rounded reciprocal and one
+// residual step (Markstein, "Computation of elementary functions on the IBM
+// RISC System/6000 processor", 1990): u = v y, u + (v - u s) y with y = 1/s.
+// bf16 inputs often make v / s a tie between two codes, so the plain product
+// v y, off by an ulp, would round a few codes in a thousand the other way.
+__device__ __forceinline__ float fb_quotient(float v, const FbScale &f) {
+  const float u = v * f.inv;
+  return fmaf(fmaf(-u, f.sr, v), f.inv, u);
+}
+
+// Four values -> four E4M3 codes, element 0 in the low byte.
+__device__ __forceinline__ uint32_t fb_codes4(float v0, float v1, float v2, float v3,
+                                              const FbScale &f) {
+  const float u0 = fb_quotient(v0, f), u1 = fb_quotient(v1, f);
+  const float u2 = fb_quotient(v2, f), u3 = fb_quotient(v3, f);
+  uint32_t r;
+  asm("{\n\t.reg .b16 lo, hi;\n\t"
+      "cvt.rn.satfinite.e4m3x2.f32 lo, %2, %1;\n\t"
+      "cvt.rn.satfinite.e4m3x2.f32 hi, %4, %3;\n\t"
+      "mov.b32 %0, {lo, hi};\n\t}"
+      : "=r"(r)
+      : "f"(u0), "f"(u1), "f"(u2), "f"(u3));
+  return r;
+}
+
+// SiLU(a) * u.  __expf and the approximate division are within a few ulp for
+// |a| < 88 (far inside the 2^-4 step of a code or the 2^-8 of bf16); below
+// -88 the quotient goes to -0, SiLU's limit there.
+__device__ __forceinline__ float fb_silu_mul(float a, float u) {
+  return __fdividef(a, 1.0f + __expf(-a)) * u;
+}
+
+// ---- thread-block clusters
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+
+__device__ __forceinline__ void cluster_sync_all() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\t"
+               "barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// Address of the same shared-memory location in CTA `rank` of the cluster.
+__device__ __forceinline__ uint32_t cluster_map(uint32_t saddr, uint32_t rank) {
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(saddr), "r"(rank));
+  return r;
+}
+
+__device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(addr)
+               : "memory");
+  return v;
+}
+
+// ---- the products' arguments
+
+struct FbMaps {
+  CUtensorMap x;     // activation codes [M][K]
+  CUtensorMap w[2];  // weight codes [N][K] (gate and up, or one matrix)
+};
+
+struct FbParams {
+  const float *sx;     // [G][M]
+  const float *sw[2];  // [ceil(N / 128)][G]
+  uint16_t *y;         // [M][N] bf16, or nullptr when the output is quantised
+  uint8_t *qh;         // [M][N] codes
+  float *sh;           // [ceil(N / 128)][M]
+  unsigned *err;
+  int M, N, G;
+  int stages;
+};
+
+// kernels of fp8_block_quant.cu / fp8_block_small.cu
+cudaError_t launch_fb_quant(const void *x, void *q, float *s, int M, int K, unsigned *err,
+                            cudaStream_t st, bool pdl);
+cudaError_t launch_fb_norm(const void *x, const void *res, const void *gamma, float eps,
+                           void *res_out, void *q, float *s, int M, int D, unsigned *err,
+                           cudaStream_t st, bool pdl);
+constexpr int FB_NORM_MAX_D = 32768  /* 4 chunks of 8 in each of 1024 threads */;
+
+const void *fb_small_kernel(int nmat, int bn);
+int fb_small_threads(int nmat, int bn);
+int fb_small_smem(int nmat, int bn, int stages);
+
+}  // namespace dfk

@@ -1,0 +1,161 @@
+// fp8_block_api.cu -- the entry points of the block-scaled FP8 operators:
+// argument checks, the choice of kernel, the launches.  Declarations and
+// argument contracts: include/dfk.h.
+#include <algorithm>
+#include <cmath>
+#include <cstring>
+
+#include "api_internal.h"
+#include "dfk.h"
+#include "fp8_block.cuh"
+#include "launch_util.h"
+
+namespace dfk {
+
+static bool off16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) != 0; }
+static bool off4(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 3u) != 0; }
+
+static int check_rows(int M, int K) {
+  if (M < 0 || K <= 0) return api_fail(DFK_ERR_INVALID_ARG, "negative or zero size");
+  if (K % 16) return api_fail(DFK_ERR_UNSUPPORTED_SHAPE, "row length %% 16 != 0 (%d)", K);
+  return DFK_OK;
+}
+
+constexpr int FB_SMEM_MAX = 232448;     // bytes a CTA may use
+constexpr int FB_SMEM_HALF = 115712;    // two CTAs on an SM
+
+struct FbCall {
+  int nmat;
+  const void *qx;
+  const float *sx;
+  const void *qw[2];
+  const float *sw[2];
+  void *y, *qh;
+  float *sh;
+  int M, K, N;
+};
+
+static int launch_small(const FbCall &c, int sms, unsigned *err, cudaStream_t st) {
+  const int G = (c.K + FB_GROUP - 1) / FB_GROUP;
+  const int bn = c.M <= 16 ? 16 : c.M <= 32 ? 32 : 64;
+  const int blocks = (c.N + 127) / 128, tiles = (c.M + bn - 1) / bn;
+  if (tiles > 65535) return api_fail(DFK_ERR_UNSUPPORTED_SHAPE, "M=%d is too large", c.M);
+  // as many CTAs per row block as fill the SMs, each with two groups or more
+  long long ks = sms / (static_cast<long long>(blocks) * tiles);
+  ks = std::max(1LL, std::min(ks, std::min(8LL, static_cast<long long>(G / 2))));
+  const bool one_wave = static_cast<long long>(blocks) * tiles * ks <= sms;
+  const int cap = one_wave ? FB_SMEM_MAX : FB_SMEM_HALF;
+  int stages = 2;
+  const int most = static_cast<int>((G + ks - 1) / ks);
+  while (stages < 16 && stages < std::max(most, 2) &&
+         fb_small_smem(c.nmat, bn, stages + 1) <= cap)
+    ++stages;
+  const void *fn = fb_small_kernel(c.nmat, bn);
+  int rc = api_allow_smem(fn);
+  if (rc) return rc;
+  FbMaps maps;
+  memset(&maps, 0, sizeof maps);
+  if ((rc = api_tensor_map_u8(c.qx, c.K, c.M, c.K, 128, bn, &maps.x))) return rc;
+  for (int m = 0; m < c.nmat; ++m)
+    if ((rc = api_tensor_map_u8(c.qw[m], c.K, c.N, c.K, 128, 128, &maps.w[m]))) return rc;
+  FbParams p{c.sx, {c.sw[0], c.sw[1]}, static_cast<uint16_t *>(c.y),
+             static_cast<uint8_t *>(c.qh), c.sh, err, c.M, c.N, G, stages};
+  void *args[] = {&maps, &p};
+  const cudaError_t e = launch_kernel(
+      fn, dim3(static_cast<unsigned>(blocks * ks), tiles), dim3(fb_small_threads(c.nmat, bn)),
+      fb_small_smem(c.nmat, bn, stages), st, api_pdl(), args, static_cast<unsigned>(ks));
+  if (e != cudaSuccess) return api_cuda_error(e, "block-scaled FP8 product launch");
+  return DFK_OK;
+}
+
+static int product(const FbCall &c, cudaStream_t st) {
+  int rc = check_rows(c.M, c.K);
+  if (rc) return rc;
+  if (c.N <= 0) return api_fail(DFK_ERR_INVALID_ARG, "negative or zero size");
+  if (c.qh || c.sh) {
+    if (c.y) return api_fail(DFK_ERR_INVALID_ARG, "both a bf16 and a quantised output");
+    if (c.N % 16)
+      return api_fail(DFK_ERR_UNSUPPORTED_SHAPE, "quantised output: row length %% 16 != 0 (%d)",
+                      c.N);
+  }
+  if (c.M == 0) return DFK_OK;
+  if (!c.qx || !c.sx || !(c.y || (c.qh && c.sh)))
+    return api_fail(DFK_ERR_INVALID_ARG, "null pointer argument");
+  if (off16(c.qx) || off16(c.y) || off16(c.qh))
+    return api_fail(DFK_ERR_MISALIGNED, "device pointers must be 16-byte aligned");
+  if (off4(c.sx) || off4(c.sh))
+    return api_fail(DFK_ERR_MISALIGNED, "scale pointers must be 4-byte aligned");
+  for (int m = 0; m < c.nmat; ++m) {
+    if (!c.qw[m] || !c.sw[m]) return api_fail(DFK_ERR_INVALID_ARG, "null pointer argument");
+    if (off16(c.qw[m]))
+      return api_fail(DFK_ERR_MISALIGNED, "device pointers must be 16-byte aligned");
+    if (off4(c.sw[m]))
+      return api_fail(DFK_ERR_MISALIGNED, "scale pointers must be 4-byte aligned");
+  }
+  int sms;
+  unsigned *err;
+  if ((rc = api_device(&sms, &err))) return rc;
+  return launch_small(c, sms, err, st);
+}
+
+}  // namespace dfk
+
+using namespace dfk;
+
+extern "C" {
+
+int dfk_quant_fp8_block(const void *x, void *q, float *s, int M, int K, void *stream) {
+  int rc = check_rows(M, K);
+  if (rc || M == 0) return rc;
+  if (!x || !q || !s) return api_fail(DFK_ERR_INVALID_ARG, "null pointer argument");
+  if (off16(x) || off16(q))
+    return api_fail(DFK_ERR_MISALIGNED, "device pointers must be 16-byte aligned");
+  if (off4(s)) return api_fail(DFK_ERR_MISALIGNED, "scale pointers must be 4-byte aligned");
+  int sms;
+  unsigned *err;
+  if ((rc = api_device(&sms, &err))) return rc;
+  const cudaError_t e =
+      launch_fb_quant(x, q, s, M, K, err, static_cast<cudaStream_t>(stream), api_pdl());
+  return e == cudaSuccess ? DFK_OK : api_cuda_error(e, "block quantisation launch");
+}
+
+int dfk_add_rmsnorm_fp8_block(const void *x, const void *residual, const void *gamma, float eps,
+                              void *residual_out, void *q, float *s, int M, int d_model,
+                              void *stream) {
+  int rc = check_rows(M, d_model);
+  if (rc) return rc;
+  if (!(eps >= 0.f && std::isfinite(eps)))
+    return api_fail(DFK_ERR_INVALID_ARG, "eps must be finite and >= 0");
+  if (d_model > FB_NORM_MAX_D)
+    return api_fail(DFK_ERR_UNSUPPORTED_SHAPE, "d_model=%d > %d", d_model, FB_NORM_MAX_D);
+  if (M == 0) return DFK_OK;
+  if (!x || !gamma || !q || !s || (residual && !residual_out))
+    return api_fail(DFK_ERR_INVALID_ARG, "null pointer argument");
+  if (!residual && residual_out)
+    return api_fail(DFK_ERR_INVALID_ARG, "residual_out without a residual");
+  if (off16(x) || off16(residual) || off16(gamma) || off16(residual_out) || off16(q))
+    return api_fail(DFK_ERR_MISALIGNED, "device pointers must be 16-byte aligned");
+  if (off4(s)) return api_fail(DFK_ERR_MISALIGNED, "scale pointers must be 4-byte aligned");
+  int sms;
+  unsigned *err;
+  if ((rc = api_device(&sms, &err))) return rc;
+  const cudaError_t e = launch_fb_norm(x, residual, gamma, eps, residual_out, q, s, M, d_model,
+                                       err, static_cast<cudaStream_t>(stream), api_pdl());
+  return e == cudaSuccess ? DFK_OK : api_cuda_error(e, "RMSNorm quantisation launch");
+}
+
+int dfk_gemm_fp8_block(const void *q_x, const float *s_x, const void *q_w, const float *s_w,
+                       void *y, int M, int K, int N, void *stream) {
+  const FbCall c{1, q_x, s_x, {q_w, nullptr}, {s_w, nullptr}, y, nullptr, nullptr, M, K, N};
+  return product(c, static_cast<cudaStream_t>(stream));
+}
+
+int dfk_swiglu_gate_up_fp8_block(const void *q_x, const float *s_x, const void *q_gate,
+                                 const float *s_gate, const void *q_up, const float *s_up,
+                                 void *h, void *q_h, float *s_h, int M, int d_model, int d_ff,
+                                 void *stream) {
+  const FbCall c{2, q_x, s_x, {q_gate, q_up}, {s_gate, s_up}, h, q_h, s_h, M, d_model, d_ff};
+  return product(c, static_cast<cudaStream_t>(stream));
+}
+
+}  // extern "C"

@@ -1,0 +1,335 @@
+// fp8_block_small.cu -- block-scaled FP8 products for few tokens: weight
+// streaming.  y[m][n] = sum_kb s_x[kb][m] s_w[n/128][kb] P_kb[n][m], where
+// P_kb is the product of the codes over one group of 128, exact products
+// summed in fp32 by the E4M3 tensor-core MMA.
+//
+// One CTA owns 128 weight rows (one scale block of each matrix: the MMA's M)
+// and BN tokens (its N), over all groups or, in a cluster of `ks` CTAs, over a
+// share of them.  A TMA ring carries one group per stage: 128 x 128 codes of
+// each matrix and BN x 128 activation codes.  The accumulator of a group is
+// read back from TMEM while the tensor core fills the other one (two TMEM
+// buffers), scaled by s_x s_w and added in fp32 registers: the scales change
+// every 128 steps of k, so no sum can stay in TMEM across groups.  The CTAs
+// of a cluster add their shares in rank order through distributed shared
+// memory: no scratch memory, no atomics, the same bits every time.
+#include "fp8_block.cuh"
+#include "tc_ptx.cuh"
+#include "tf8mma_engine.cuh"
+
+namespace dfk {
+
+constexpr int FBS_THREADS = 192;   // TMA warp, MMA warp, four epilogue warps
+constexpr int FBS_WTILE = 128 * 128;
+constexpr int FBS_PRE = 4;         // groups whose scales are loaded ahead
+
+template <int NMAT, int BN>
+struct FbsShape {
+  static constexpr int stage_bytes = NMAT * FBS_WTILE + BN * 128;
+  static constexpr int acc_cols = NMAT * BN;       // one TMEM buffer
+  static constexpr int tmem_cols = 2 * acc_cols < 32 ? 32 : 2 * acc_cols;
+  static constexpr int comb_floats = 4 * 2 * NMAT * BN;  // per warp, two groups
+  static constexpr int part_bytes = NMAT * BN * 128 * 4;
+};
+
+template <int NMAT, int BN>
+__global__ void __launch_bounds__(FBS_THREADS)
+    fb_small_kernel_t(const __grid_constant__ FbMaps maps, const FbParams p) {
+  using Sh = FbsShape<NMAT, BN>;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  const uint32_t raw_addr = smem_addr(smem_raw);
+  uint8_t *smem = smem_raw + ((1024u - (raw_addr & 1023u)) & 1023u);
+  const uint32_t sbase = smem_addr(smem);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int S = p.stages;
+
+  float *s_comb = reinterpret_cast<float *>(smem + static_cast<size_t>(S) * Sh::stage_bytes);
+  uint64_t *fullb = reinterpret_cast<uint64_t *>(s_comb + Sh::comb_floats);
+  uint64_t *empty = fullb + S;
+  uint64_t *accfull = empty + S;  // [2]
+  uint64_t *accempty = accfull + 2;
+  uint64_t *done = accempty + 2;
+  volatile int *s_abort = reinterpret_cast<volatile int *>(done + 1);
+  int *s_issued = reinterpret_cast<int *>(done + 1) + 1;
+  uint32_t *s_tmem = reinterpret_cast<uint32_t *>(done + 1) + 2;
+
+  // clusters of ks consecutive blocks share a row block
+  uint32_t ks;
+  asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(ks));
+  const uint32_t rank = cluster_rank();
+  const int blk = blockIdx.x / ks;
+  const int j0 = blk * 128, n0 = blockIdx.y * BN;
+  const int kb0 = static_cast<int>(static_cast<long long>(rank) * p.G / ks);
+  const int kb1 = static_cast<int>(static_cast<long long>(rank + 1) * p.G / ks);
+  const int nkb = kb1 - kb0;
+
+  if (tid == 0) {
+    for (int s = 0; s < S; ++s) {
+      mbar_init(&fullb[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&accfull[s], 1);
+      mbar_init(&accempty[s], 4);
+    }
+    mbar_init(done, 1);
+    *s_abort = 0;
+    *s_issued = 0;
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(s_tmem, Sh::tmem_cols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *s_tmem;
+  pdl_launch_dependents();
+
+  if (warp == 0) {
+    // ---- TMA: weights of the first S stages before the dependency, the
+    // activation codes after it
+    if (lane == 0) {
+      const uint64_t pol_w = gridDim.y > 1 ? l2_policy_evict_normal() : l2_policy_evict_first();
+      const uint64_t pol_x = l2_policy_evict_normal();
+      const int S0 = min(S, nkb);
+      auto load_w = [&](int i) {
+        uint8_t *sb = smem + static_cast<size_t>(i % S) * Sh::stage_bytes;
+        mbar_arrive_expect_tx(&fullb[i % S], Sh::stage_bytes);
+#pragma unroll
+        for (int m = 0; m < NMAT; ++m)
+          tma_load_2d(sb + m * FBS_WTILE, &maps.w[m], &fullb[i % S], (kb0 + i) * 128, j0, pol_w);
+      };
+      auto load_x = [&](int i) {
+        uint8_t *sb = smem + static_cast<size_t>(i % S) * Sh::stage_bytes;
+        tma_load_2d(sb + NMAT * FBS_WTILE, &maps.x, &fullb[i % S], (kb0 + i) * 128, n0, pol_x);
+      };
+      for (int i = 0; i < S0; ++i) load_w(i);
+      pdl_wait();
+      for (int i = 0; i < S0; ++i) load_x(i);
+      int issued = S0;
+      for (int i = S0; i < nkb; ++i) {
+        if (!mbar_wait_bounded(&empty[i % S], ((i / S) - 1) & 1, s_abort, p.err)) break;
+        load_w(i);
+        load_x(i);
+        issued = i + 1;
+      }
+      *s_issued = issued;
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    // ---- MMA: 4 instructions of K = 32 per matrix and group
+    const uint32_t leader = elect_one_sync();
+    const uint32_t idesc = umma_idesc_e4m3_f32(128, BN);
+    const uint64_t desc0 = umma_desc_sw128(sbase);
+    for (int i = 0; i < nkb; ++i) {
+      const int st = i % S, ab = i & 1;
+      bool ok = mbar_wait_bounded(&fullb[st], (i / S) & 1, s_abort, p.err);
+      if (ok && i >= 2) ok = mbar_wait_bounded(&accempty[ab], ((i >> 1) - 1) & 1, s_abort, p.err);
+      if (!__all_sync(0xffffffffu, ok)) break;
+      tc_fence_after();
+      const uint64_t ds = desc0 + (static_cast<uint32_t>(st * Sh::stage_bytes) >> 4);
+      const uint64_t bx = ds + (static_cast<uint32_t>(NMAT * FBS_WTILE) >> 4);
+#pragma unroll
+      for (int m = 0; m < NMAT; ++m)
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk)
+          if (leader)
+            umma_e4m3(tmem + static_cast<uint32_t>(ab * Sh::acc_cols + m * BN),
+                      ds + m * (FBS_WTILE >> 4) + 2 * kk, bx + 2 * kk, idesc, kk > 0 ? 1u : 0u);
+      if (leader) {
+        umma_commit(&empty[st]);
+        umma_commit(&accfull[ab]);
+      }
+      __syncwarp();
+    }
+    if (leader) umma_commit(done);
+    __syncwarp();
+  } else {
+    // ---- epilogue warps 2..5: TMEM lane quarter = warp mod 4
+    const int ew = warp - 2, q = warp & 3;
+    const int row = 32 * q + lane;
+    const uint32_t base = tmem + (static_cast<uint32_t>(32 * q) << 16);
+    constexpr int SL = (BN + 31) / 32;  // tokens a lane loads scales for
+    float *comb = s_comb + ew * 2 * NMAT * BN;
+    float acc[NMAT][BN];
+#pragma unroll
+    for (int m = 0; m < NMAT; ++m)
+#pragma unroll
+      for (int n = 0; n < BN; ++n) acc[m][n] = 0.f;
+    float psx[FBS_PRE][SL], psw[FBS_PRE][NMAT];
+    pdl_wait();  // s_x comes from the previous kernel
+    auto fetch = [&](int i, float (&sx)[SL], float (&sw)[NMAT]) {
+      const int kb = kb0 + i;
+#pragma unroll
+      for (int m = 0; m < NMAT; ++m)
+        sw[m] = i < nkb ? __ldg(p.sw[m] + static_cast<size_t>(blk) * p.G + kb) : 0.f;
+#pragma unroll
+      for (int e = 0; e < SL; ++e) {
+        const int n = n0 + lane + 32 * e;
+        sx[e] = 0.f;
+        if (i < nkb && lane + 32 * e < BN && n < p.M && DFK_IN_BOUNDS(kb < p.G, 27, p.err))
+          sx[e] = __ldg(p.sx + static_cast<size_t>(kb) * p.M + n);
+      }
+    };
+#pragma unroll
+    for (int u = 0; u < FBS_PRE; ++u) fetch(u, psx[u], psw[u]);
+    bool go = true;
+    for (int i0 = 0; go && i0 < nkb; i0 += FBS_PRE) {
+#pragma unroll
+      for (int u = 0; u < FBS_PRE; ++u) {
+        const int i = i0 + u;
+        if (go && i < nkb) {
+          const int ab = u & 1;  // FBS_PRE is even: the same as i & 1
+          // this group's s_x s_w, one per token, for the whole warp
+          float *cb = comb + ab * NMAT * BN;
+#pragma unroll
+          for (int m = 0; m < NMAT; ++m)
+#pragma unroll
+            for (int e = 0; e < SL; ++e)
+              if (BN >= 32 || lane < BN) cb[m * BN + lane + 32 * e] = psx[u][e] * psw[u][m];
+          fetch(i + FBS_PRE, psx[u], psw[u]);
+          __syncwarp();
+          go = __all_sync(0xffffffffu, mbar_wait_bounded(&accfull[ab], (i >> 1) & 1, s_abort,
+                                                         p.err));
+          if (go) {
+            tc_fence_after();
+#pragma unroll
+            for (int m = 0; m < NMAT; ++m)
+#pragma unroll
+              for (int c = 0; c < BN; c += 16) {
+                float d[16];
+                tmem_ld_32x32b_x16(base + ab * Sh::acc_cols + m * BN + c, d);
+                tmem_ld_wait();
+#pragma unroll
+                for (int e = 0; e < 16; e += 4) {
+                  const float4 w = *reinterpret_cast<const float4 *>(cb + m * BN + c + e);
+                  acc[m][c + e + 0] = fmaf(d[e + 0], w.x, acc[m][c + e + 0]);
+                  acc[m][c + e + 1] = fmaf(d[e + 1], w.y, acc[m][c + e + 1]);
+                  acc[m][c + e + 2] = fmaf(d[e + 2], w.z, acc[m][c + e + 2]);
+                  acc[m][c + e + 3] = fmaf(d[e + 3], w.w, acc[m][c + e + 3]);
+                }
+              }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&accempty[ab]);
+          }
+        }
+      }
+    }
+    // every MMA has read its stage by now: the ring holds the partial sums
+    // [matrix][token][row]
+    float *part = reinterpret_cast<float *>(smem);
+    if (go)
+#pragma unroll
+      for (int m = 0; m < NMAT; ++m)
+#pragma unroll
+        for (int n = 0; n < BN; ++n) part[(m * BN + n) * 128 + row] = acc[m][n];
+  }
+
+  // TMEM is released and the copies in flight are waited for before the
+  // cluster meets (after an abort; normally all have been consumed)
+  __syncthreads();
+  if (warp == 1) {
+    if (lane == 0) mbar_wait_bounded(done, 0, nullptr, p.err);
+    __syncwarp();
+    tc_fence_after();
+    tmem_dealloc(tmem, Sh::tmem_cols);
+  }
+  if (tid == 0 && *s_abort) {
+    const int issued = *s_issued;
+    for (int st = 0; st < S; ++st) {
+      int last = -1;
+      for (int i = issued - 1; i >= 0 && i >= issued - S; --i)
+        if (i % S == st) { last = i; break; }
+      if (last >= 0) mbar_wait_bounded(&fullb[st], (last / S) & 1, nullptr, p.err);
+    }
+  }
+  __syncwarp();
+  if (ks > 1) cluster_sync_all();
+  if (warp >= 2 && !*s_abort) {
+    // one token per warp and turn, spread over the cluster's CTAs; lane l
+    // takes rows 4 l .. 4 l + 3
+    const int nt = min(BN, p.M - n0);
+    for (int n = rank * 4 + (warp - 2); n < nt; n += 4 * ks) {
+      float a[NMAT][4];
+#pragma unroll
+      for (int m = 0; m < NMAT; ++m) {
+        const uint32_t at = sbase + static_cast<uint32_t>(((m * BN + n) * 128 + 4 * lane) * 4);
+        float4 t = ld_cluster_f4(cluster_map(at, 0));
+        for (uint32_t r = 1; r < ks; ++r) {
+          const float4 o = ld_cluster_f4(cluster_map(at, r));
+          t.x += o.x;
+          t.y += o.y;
+          t.z += o.z;
+          t.w += o.w;
+        }
+        a[m][0] = t.x;
+        a[m][1] = t.y;
+        a[m][2] = t.z;
+        a[m][3] = t.w;
+      }
+      const int j = j0 + 4 * lane;
+      float h[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        if (NMAT == 2) h[e] = fb_silu_mul(a[0][e], a[NMAT - 1][e]);
+        else h[e] = a[0][e];
+        if (j + e >= p.N) h[e] = 0.f;
+      }
+      const size_t at = static_cast<size_t>(n0 + n) * p.N + j;
+      if (NMAT == 2 && p.y == nullptr) {
+        float mx = max_nan(max_nan(fabsf(h[0]), fabsf(h[1])), max_nan(fabsf(h[2]), fabsf(h[3])));
+#pragma unroll
+        for (int d = 16; d >= 1; d >>= 1) mx = max_nan(mx, __shfl_xor_sync(0xffffffffu, mx, d));
+        const FbScale f = fb_scale(mx);
+        if (j < p.N && DFK_IN_BOUNDS(j + 4 <= p.N && n0 + n < p.M, 28, p.err))
+          *reinterpret_cast<uint32_t *>(p.qh + at) = fb_codes4(h[0], h[1], h[2], h[3], f);
+        if (lane == 0) p.sh[static_cast<size_t>(blk) * p.M + n0 + n] = f.s;
+      } else if ((p.N & 3) == 0) {
+        if (j < p.N && DFK_IN_BOUNDS(j + 4 <= p.N && n0 + n < p.M, 29, p.err))
+          *reinterpret_cast<uint2 *>(p.y + at) =
+              make_uint2(f32_to_bf16_bits(h[0]) | (static_cast<uint32_t>(f32_to_bf16_bits(h[1])) << 16),
+                         f32_to_bf16_bits(h[2]) | (static_cast<uint32_t>(f32_to_bf16_bits(h[3])) << 16));
+      } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (j + e < p.N && DFK_IN_BOUNDS(n0 + n < p.M, 30, p.err))
+            p.y[at + e] = f32_to_bf16_bits(h[e]);
+      }
+    }
+  }
+  __syncwarp();
+  if (ks > 1) cluster_sync_all();  // no CTA leaves while its sums are being read
+}
+
+template <int NMAT, int BN>
+static int smem_of(int stages) {
+  using Sh = FbsShape<NMAT, BN>;
+  const int ring = stages * Sh::stage_bytes;
+  return 1024 + ring + Sh::comb_floats * 4 + (2 * stages + 5) * 8 + 16;
+}
+
+#define DFK_FBS_PICK(expr)                                   \
+  (nmat == 1 ? (bn == 16   ? expr(1, 16)                     \
+                : bn == 32 ? expr(1, 32)                     \
+                           : expr(1, 64))                    \
+             : (bn == 16   ? expr(2, 16)                     \
+                : bn == 32 ? expr(2, 32)                     \
+                           : expr(2, 64)))
+
+const void *fb_small_kernel(int nmat, int bn) {
+#define DFK_FBS_FN(NM, B) reinterpret_cast<const void *>(&fb_small_kernel_t<NM, B>)
+  return DFK_FBS_PICK(DFK_FBS_FN);
+#undef DFK_FBS_FN
+}
+
+int fb_small_threads(int, int) { return FBS_THREADS; }
+
+int fb_small_smem(int nmat, int bn, int stages) {
+#define DFK_FBS_SM(NM, B) smem_of<NM, B>(stages)
+  return DFK_FBS_PICK(DFK_FBS_SM);
+#undef DFK_FBS_SM
+}
+
+}  // namespace dfk

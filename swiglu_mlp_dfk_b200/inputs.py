@@ -171,6 +171,19 @@ def to_fp8_rows(w: torch.Tensor):
     return q, s.contiguous()
 
 
+def to_fp8_blocks(w: torch.Tensor):
+    """FP8 E4M3 weights with one fp32 scale per 128 x 128 block, from weights [N, K]:
+    s = max(max|w| / 448, 2^-126) per block, Q = E4M3(w / s).  Returns (Q as float8_e4m3fn
+    [N, K], s float32 [ceil(N / 128), ceil(K / 128)])."""
+    N, K = w.shape
+    gn, gk = -(-N // 128), -(-K // 128)
+    b = torch.nn.functional.pad(w.float(), (0, gk * 128 - K, 0, gn * 128 - N))
+    b = b.view(gn, 128, gk, 128)
+    s = (b.abs().amax((1, 3)) / 448.0).clamp(min=2.0 ** -126)
+    q = (b / s[:, None, :, None]).to(torch.float8_e4m3fn).view(gn * 128, gk * 128)
+    return q[:N, :K].contiguous(), s.contiguous()
+
+
 def fp8_values(q: torch.Tensor) -> np.ndarray:
     """Exact float64 values of E4M3 codes (bit-level conversion through torch)."""
     return q.detach().contiguous().view(torch.float8_e4m3fn).float().cpu().numpy().astype(

@@ -1,0 +1,108 @@
+"""Refusals of the block-scaled FP8 operators, checked before any GPU work (fake addresses that
+are never dereferenced), and the weight encoder."""
+import ctypes
+
+import pytest
+import torch
+
+import swiglu_mlp_dfk_b200 as dfk
+from swiglu_mlp_dfk_b200 import inputs as I
+
+
+@pytest.fixture(scope="module")
+def L():
+    from swiglu_mlp_dfk_b200 import build
+    build.build()
+    return dfk.lib()
+
+
+P, P2, P3, P4, P5, P6 = (ctypes.c_void_p(0x10000 * (i + 1)) for i in range(6))
+MIS = ctypes.c_void_p(0x10008)   # not 16-byte aligned
+ODD = ctypes.c_void_p(0x10002)   # not 4-byte aligned
+BAD, SHAPE, ALIGN = dfk.DFK_ERR_INVALID_ARG, dfk.DFK_ERR_UNSUPPORTED_SHAPE, dfk.DFK_ERR_MISALIGNED
+
+
+def quant(L, x=P, q=P2, s=P3, M=1, K=128):
+    return L.dfk_quant_fp8_block(x, q, s, M, K, None)
+
+
+def norm(L, x=P, res=P2, gamma=P3, eps=1e-5, out=P4, q=P5, s=P6, M=1, D=128):
+    return L.dfk_add_rmsnorm_fp8_block(x, res, gamma, eps, out, q, s, M, D, None)
+
+
+def gemm(L, qx=P, sx=P2, qw=P3, sw=P4, y=P5, M=1, K=128, N=128):
+    return L.dfk_gemm_fp8_block(qx, sx, qw, sw, y, M, K, N, None)
+
+
+def gate_up(L, qx=P, sx=P2, qg=P3, sg=P4, qu=P3, su=P4, h=None, qh=P5, sh=P6, M=1, D=128, F=128):
+    return L.dfk_swiglu_gate_up_fp8_block(qx, sx, qg, sg, qu, su, h, qh, sh, M, D, F, None)
+
+
+@pytest.mark.parametrize("fn,kw,status", [
+    (quant, dict(M=-1), BAD), (quant, dict(K=0), BAD), (quant, dict(K=24), SHAPE),
+    (quant, dict(x=None), BAD), (quant, dict(q=None), BAD), (quant, dict(s=None), BAD),
+    (quant, dict(x=MIS), ALIGN), (quant, dict(q=MIS), ALIGN), (quant, dict(s=ODD), ALIGN),
+    (norm, dict(M=-1), BAD), (norm, dict(D=-16), BAD), (norm, dict(D=120), SHAPE),
+    (norm, dict(D=32784), SHAPE), (norm, dict(eps=-1.0), BAD), (norm, dict(eps=float("nan")), BAD),
+    (norm, dict(eps=float("inf")), BAD), (norm, dict(x=None), BAD), (norm, dict(gamma=None), BAD),
+    (norm, dict(out=None), BAD), (norm, dict(res=None), BAD), (norm, dict(q=None), BAD),
+    (norm, dict(s=None), BAD), (norm, dict(res=MIS), ALIGN), (norm, dict(out=MIS), ALIGN),
+    (norm, dict(gamma=MIS), ALIGN), (norm, dict(s=ODD), ALIGN),
+    (gemm, dict(M=-1), BAD), (gemm, dict(N=0), BAD), (gemm, dict(K=8), SHAPE),
+    (gemm, dict(qx=None), BAD), (gemm, dict(sx=None), BAD), (gemm, dict(qw=None), BAD),
+    (gemm, dict(sw=None), BAD), (gemm, dict(y=None), BAD), (gemm, dict(qx=MIS), ALIGN),
+    (gemm, dict(qw=MIS), ALIGN), (gemm, dict(y=MIS), ALIGN), (gemm, dict(sx=ODD), ALIGN),
+    (gemm, dict(sw=ODD), ALIGN),
+    (gate_up, dict(M=-1), BAD), (gate_up, dict(F=0), BAD), (gate_up, dict(D=8), SHAPE),
+    (gate_up, dict(F=24), SHAPE), (gate_up, dict(h=P5), BAD), (gate_up, dict(qh=None), BAD),
+    (gate_up, dict(sh=None), BAD), (gate_up, dict(qh=None, sh=None), BAD),
+    (gate_up, dict(qu=None), BAD), (gate_up, dict(su=None), BAD), (gate_up, dict(qg=MIS), ALIGN),
+    (gate_up, dict(qu=MIS), ALIGN), (gate_up, dict(qh=MIS), ALIGN), (gate_up, dict(sh=ODD), ALIGN),
+    (gate_up, dict(su=ODD), ALIGN), (gate_up, dict(h=MIS, qh=None, sh=None), ALIGN),
+])
+def test_refusals(L, fn, kw, status):
+    assert fn(L, **kw) == status
+    assert L.dfk_last_error().decode()
+
+
+def test_no_tokens_is_a_no_op(L):
+    assert quant(L, x=None, M=0) == 0
+    assert norm(L, x=None, M=0) == 0
+    assert gemm(L, qx=None, M=0) == 0
+    assert gate_up(L, qx=None, M=0) == 0
+
+
+@pytest.mark.skipif(torch.cuda.is_available(), reason="checks the behaviour without a device")
+def test_valid_calls_fail_loudly_without_a_device(L):
+    for fn in (quant, norm, gemm, gate_up):
+        assert fn(L) == dfk.DFK_ERR_ARCH
+
+
+def test_binding_refuses_host_tensors():
+    x = torch.zeros(2, 128, dtype=torch.bfloat16)
+    for call in (lambda: dfk.dfk_quant_fp8_block(x),
+                 lambda: dfk.dfk_add_rmsnorm_fp8_block(x, None, x[0], 1e-5),
+                 lambda: dfk.dfk_gemm_fp8_block(x, x, x, x),
+                 lambda: dfk.dfk_swiglu_gate_up_fp8_block(x, x, x, x, x, x)):
+        with pytest.raises(dfk.DfkError) as e:
+            call()
+        assert e.value.status == BAD
+
+
+@pytest.mark.parametrize("N,K", [(1, 16), (128, 128), (129, 144), (300, 272)])
+def test_weight_encoder(N, K):
+    g = torch.Generator().manual_seed(N)
+    w = torch.randn(N, K, generator=g)
+    w[: min(N, 128), :128] = 0          # an all-zero block
+    q, s = I.to_fp8_blocks(w)
+    assert q.shape == (N, K) and q.dtype == torch.float8_e4m3fn
+    assert s.shape == (-(-N // 128), -(-K // 128)) and s.dtype == torch.float32
+    assert s[0, 0] == 2.0 ** -126 and (q[:128, :128].float() == 0).all()
+    sf = s.double().repeat_interleave(128, 0)[:N].repeat_interleave(128, 1)[:, :K]
+    err = (q.double() * sf - w.double()).abs()
+    # half a step of E4M3: 2^-4 of the value, or 2^-10 of the scale below the normal range
+    assert (err <= torch.maximum(w.double().abs() * 2.0 ** -4, sf * 2.0 ** -10) * (1 + 1e-6)).all()
+    for i in range(s.shape[0]):
+        for j in range(s.shape[1]):
+            top = w[128 * i:128 * i + 128, 128 * j:128 * j + 128].abs().max()
+            assert s[i, j] == max((top / 448).item(), 2.0 ** -126)

@@ -1,0 +1,490 @@
+"""The block-scaled FP8 operators on the GPU against their definitions in 64 bits.
+
+Tolerances, from the arithmetic:
+  * a rounding is off by at most half a step: bf16 2^-8 of the value, E4M3 2^-4 of the value or,
+    below its normal range, 2^-10 of the scale;
+  * a product over groups of 128 in fp32: each of a group's 128 exact products enters the sum with
+    at most one step 2^-23 of error, then each of the G groups is scaled (two roundings) and added
+    (one): together (128 * 2^-23 + (G + 3) * 2^-24) times the sum of the terms' magnitudes;
+  * SiLU's slope is below 1.1; __expf is within 2 + 1.2 |a| steps 2^-23 and the quotient and the
+    product a few: (8 + 2 |a|) 2^-23 of the value.
+"""
+import os
+import subprocess
+import sys
+
+import pytest
+import torch
+
+import swiglu_mlp_dfk_b200 as dfk
+from swiglu_mlp_dfk_b200 import inputs as I
+
+pytestmark = pytest.mark.gpu
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+E4M3 = torch.float8_e4m3fn
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("needs a CUDA device")
+    from swiglu_mlp_dfk_b200 import build
+    build.build()
+    dfk.dfk_device_error()
+    yield
+    torch.cuda.synchronize()
+    assert dfk.dfk_device_error() == 0
+
+
+def gen(seed):
+    g = torch.Generator(device="cuda")
+    g.manual_seed(seed)
+    return g
+
+
+def rand_bf16(g, *shape, std=1.0):
+    return (std * torch.randn(*shape, generator=g, device="cuda")).bfloat16()
+
+
+def spread(q, s, dim_rows):
+    """Scales of codes as a full matrix: s [G, M] (activations) or [N/128, G] (weights)."""
+    M, K = q.shape
+    s = s.double()
+    s = s.t() if dim_rows else s.repeat_interleave(128, 0)[:M]
+    return s.repeat_interleave(128, 1)[:, :K]
+
+
+def values(q, s, activations=True):
+    return q.view(E4M3).double() * spread(q, s, activations)
+
+
+def activations(g, M, K):
+    """8-bit activations made by plain torch operations."""
+    G = -(-K // 128)
+    x = torch.randn(M, K, generator=g, device="cuda") * \
+        torch.exp(torch.randn(M, 1, generator=g, device="cuda"))
+    p = torch.nn.functional.pad(x, (0, G * 128 - K)).view(M, G, 128)
+    s = (p.abs().amax(2) / 448).clamp(min=2.0 ** -126)
+    q = (p / s[:, :, None]).clamp(-448, 448).to(E4M3).view(M, -1)[:, :K].contiguous()
+    return q, s.t().contiguous()
+
+
+def weights(g, N, K, std=0.05):
+    return I.to_fp8_blocks(std * torch.randn(N, K, generator=g, device="cuda"))
+
+
+def sum_error(G):
+    return 128 * 2.0 ** -23 + (G + 3) * 2.0 ** -24
+
+
+def product(q_x, s_x, q_w, s_w):
+    """(x W^T, its error bound) in 64 bits."""
+    x, w = values(q_x, s_x), values(q_w, s_w, False)
+    return x @ w.t(), sum_error(s_x.shape[0]) * (x.abs() @ w.abs().t())
+
+
+def check_rounded(y, ref, err, step):
+    bad = (y.double() - ref).abs() > step * ref.abs() + err * (1 + step)
+    assert not bad.any(), (int(bad.sum()), float((y.double() - ref).abs().max()))
+
+
+def check_quantised(q, s, ref, err):
+    """Codes and scales against the unrounded values `ref`, known to within `err`."""
+    M, K = ref.shape
+    G = -(-K // 128)
+    pad = (0, G * 128 - K)
+    top = torch.nn.functional.pad(ref.abs(), pad).view(M, G, 128).amax(2).t()
+    off = torch.nn.functional.pad(err, pad).view(M, G, 128).amax(2).t()
+    want = (top / 448).clamp(min=2.0 ** -126)
+    assert ((s.double() - want).abs() <= off / 448 + 2.0 ** -23 * want).all()
+    got, sf = values(q, s), spread(q, s, True)
+    half = torch.maximum(2.0 ** -4 * ref.abs(), 2.0 ** -10 * sf)
+    bad = (got - ref).abs() > half * (1 + 2.0 ** -20) + err * (1 + 2.0 ** -3)
+    assert not bad.any(), (int(bad.sum()), float((got - ref).abs().max()))
+
+
+def silu_mul(a, ea, u, eu):
+    """SiLU(a) * u in 64 bits and how far it may be off."""
+    f = a * torch.sigmoid(a)
+    return f * u, 1.1 * ea * (u.abs() + eu) + f.abs() * eu + \
+        (8 + 2 * a.abs()) * 2.0 ** -23 * (f * u).abs()
+
+
+# ---- quantisation
+
+def quant_reference(x):
+    """Bitwise: fp32 division is correctly rounded on both sides."""
+    M, K = x.shape
+    G = -(-K // 128)
+    p = torch.nn.functional.pad(x.float().cpu(), (0, G * 128 - K)).view(M, G, 128)
+    s = (p.abs().amax(2) / 448).clamp(min=2.0 ** -126)
+    q = (p / s[:, :, None]).clamp(-448, 448).to(E4M3).view(M, -1)[:, :K]
+    return q.contiguous(), s.t().contiguous()
+
+
+@pytest.mark.parametrize("M,K", [(1, 16), (1, 4096), (2, 112), (3, 128), (4, 144), (5, 2064),
+                                 (7, 14336), (33, 688), (130, 256), (257, 1040), (1000, 272)])
+def test_quant(M, K):
+    x = rand_bf16(gen(M * 10000 + K), M, K)
+    q, s = dfk.dfk_quant_fp8_block(x)
+    wq, ws = quant_reference(x)
+    assert torch.equal(s.cpu(), ws)
+    assert torch.equal(q.cpu().view(torch.uint8), wq.view(torch.uint8))
+
+
+def test_quant_every_bf16_pair_of_magnitudes():
+    """Every positive bf16 mantissa against every largest-element mantissa: all the ties."""
+    a = (torch.arange(128, dtype=torch.float64) / 128 + 1)
+    x = torch.empty(128 * 8, 128, dtype=torch.float64)
+    for e in range(8):
+        x[e * 128:(e + 1) * 128, 1:] = (a[:127] * 2.0 ** -e)[None]
+        x[e * 128:(e + 1) * 128, 0] = a * 2
+    x[:, 2::2] *= -1
+    x = x.cuda().bfloat16()
+    q, s = dfk.dfk_quant_fp8_block(x)
+    wq, ws = quant_reference(x)
+    assert torch.equal(s.cpu(), ws)
+    assert torch.equal(q.cpu().view(torch.uint8), wq.view(torch.uint8))
+
+
+def test_quant_special_values():
+    x = torch.zeros(6, 384, device="cuda", dtype=torch.bfloat16)
+    x[1, :128] = 2.0 ** -133                       # the smallest bf16: scale at its floor
+    x[2, 130] = float("nan")
+    x[3, 5] = float("inf")
+    x[3, 6] = 3.0
+    x[4, 300] = torch.finfo(torch.bfloat16).max
+    x[5, :] = -1.0
+    q, s = dfk.dfk_quant_fp8_block(x)
+    f = q.float()
+    assert (s[:, 0] == 2.0 ** -126).all() and (f[0] == 0).all()
+    assert s[0, 1] == 2.0 ** -126 and (f[1, :128] == 2.0 ** -7).all()
+    assert torch.isnan(s[1, 2]) and torch.isnan(f[2, 128:256]).all()
+    assert not torch.isnan(f[2, :128]).any() and not torch.isnan(f[2, 256:]).any()
+    assert torch.isinf(s[0, 3]) and torch.isnan(f[3, 5]) and f[3, 6] == 0
+    assert f[4, 300] == 448 and torch.isfinite(s[:, 4]).all()
+    assert (f[5] == -448).all()
+
+
+# ---- norm
+
+@pytest.mark.parametrize("M,D", [(1, 16), (1, 4096), (2, 144), (3, 688), (5, 2064), (9, 4112),
+                                 (17, 8192), (300, 256), (2, 16400), (3, 32768)])
+@pytest.mark.parametrize("with_residual", [True, False])
+def test_add_rmsnorm(M, D, with_residual):
+    g = gen(M + D)
+    x, res = rand_bf16(g, M, D), rand_bf16(g, M, D, std=3.0)
+    gamma = (1 + 0.2 * torch.randn(D, generator=g, device="cuda")).bfloat16()
+    q, s, r = dfk.dfk_add_rmsnorm_fp8_block(x, res if with_residual else None, gamma, 1e-5)
+    if with_residual:
+        assert torch.equal(r, (x.float() + res.float()).bfloat16())
+    else:
+        assert r is None
+        r = x
+    d = r.double()
+    v = d / (d.square().mean(1, keepdim=True) + 1e-5).sqrt() * gamma.double()
+    # a thread chains 32 squares at most, two butterflies add 10 more, then the mean, the root,
+    # the quotient and two products: under 64 roundings of 2^-24, halved by the root
+    check_quantised(q, s, v, 2.0 ** -18 * v.abs())
+
+
+def test_add_rmsnorm_in_place_and_zero_rows():
+    g = gen(5)
+    x, res = rand_bf16(g, 4, 512), rand_bf16(g, 4, 512)
+    x[2] = 0
+    res[2] = 0
+    gamma = torch.ones(512, device="cuda").bfloat16()
+    q0, s0, r0 = dfk.dfk_add_rmsnorm_fp8_block(x, res, gamma, 1e-5)
+    assert (q0[2].float() == 0).all() and (s0[:, 2] == 2.0 ** -126).all()
+    for into in ("residual", "x"):
+        a, b = x.clone(), res.clone()
+        out = b if into == "residual" else a
+        q, s, r = dfk.dfk_add_rmsnorm_fp8_block(a, b, gamma, 1e-5, residual_out=out)
+        assert r is out and torch.equal(r, r0)
+        assert torch.equal(q.view(torch.uint8), q0.view(torch.uint8)) and torch.equal(s, s0)
+
+
+def test_add_rmsnorm_all_zero_row_with_zero_eps_is_nan_as_the_formula():
+    x = torch.zeros(2, 256, device="cuda", dtype=torch.bfloat16)
+    x[1] = 1
+    q, s, _ = dfk.dfk_add_rmsnorm_fp8_block(x, None, torch.ones_like(x[0]), 0.0)
+    assert torch.isnan(s[:, 0]).all() and torch.isnan(q[0].float()).all()   # 0 * inf
+    assert torch.isfinite(s[:, 1]).all() and (q[1].float() == 448).all()
+
+
+# ---- products
+
+SHAPES = [(1, 16, 1), (1, 128, 128), (2, 144, 130), (1, 4096, 512), (3, 2064, 1001),
+          (16, 1040, 129), (17, 256, 688), (31, 688, 256), (33, 272, 96), (64, 512, 4096),
+          (65, 512, 1032), (127, 640, 384), (128, 128, 257), (129, 1152, 640), (200, 400, 1000),
+          (255, 2064, 255), (256, 256, 256), (257, 384, 520), (300, 14336, 200), (513, 144, 768),
+          (777, 2064, 1001), (1024, 1024, 1024)]
+
+
+@pytest.mark.parametrize("M,K,N", SHAPES)
+def test_gemm(M, K, N):
+    g = gen(M * 7 + K * 3 + N)
+    q_x, s_x = activations(g, M, K)
+    q_w, s_w = weights(g, N, K)
+    y = dfk.dfk_gemm_fp8_block(q_x, s_x, q_w, s_w)
+    ref, err = product(q_x, s_x, q_w, s_w)
+    check_rounded(y, ref, err, 2.0 ** -8)
+
+
+@pytest.mark.parametrize("M,D,F", [s for s in SHAPES if s[1] < 4000 or s[0] < 100])
+@pytest.mark.parametrize("fp8_out", [True, False])
+def test_gate_up(M, D, F, fp8_out):
+    if fp8_out:
+        F = -(-F // 16) * 16
+    g = gen(M * 5 + D + F)
+    q_x, s_x = activations(g, M, D)
+    wg, wu = weights(g, F, D), weights(g, F, D)
+    out = dfk.dfk_swiglu_gate_up_fp8_block(q_x, s_x, *wg, *wu, fp8_out=fp8_out)
+    ref, err = silu_mul(*product(q_x, s_x, *wg), *product(q_x, s_x, *wu))
+    if fp8_out:
+        check_quantised(*out, ref, err)
+    else:
+        check_rounded(out, ref, err, 2.0 ** -8)
+
+
+def test_silu_far_from_zero():
+    """Gate values from -600 to 600: SiLU's limits, no overflow."""
+    M, D, F = 40, 128, 128
+    q_x = torch.zeros(M, D, device="cuda", dtype=E4M3)
+    q_x[:, 0] = 1
+    s_x = torch.linspace(-600, 600, M, device="cuda")[None].contiguous()
+    q_w = torch.ones(F, D, device="cuda").to(E4M3)
+    s_w = torch.ones(1, 1, device="cuda")
+    h = dfk.dfk_swiglu_gate_up_fp8_block(q_x, s_x, q_w, s_w, q_w, s_w / 256, fp8_out=False)
+    a = s_x[0].double()
+    ref = (a * torch.sigmoid(a) * a / 256)[:, None].expand(M, F)
+    assert torch.isfinite(h.float()).all()
+    # below -80 exp(a) leaves fp32's normal range: there SiLU * up is under 1e-30
+    assert ((h.double() - ref).abs() <= (2.0 ** -8 + 2.0 ** -12) * ref.abs() + 1e-30).all()
+
+
+def test_scales_of_every_block_count():
+    """One code per group and block: y shows which scale met which."""
+    M, K, N = 150, 656, 400
+    G, B = 6, 4
+    q_x = torch.zeros(M, K, device="cuda", dtype=E4M3)
+    q_x[:, ::128] = 1
+    q_w = torch.ones(N, K, device="cuda").to(E4M3)
+    g = gen(3)
+    s_x = torch.randn(G, M, generator=g, device="cuda").bfloat16().float()
+    s_w = torch.randn(B, G, generator=g, device="cuda").bfloat16().float()
+    y = dfk.dfk_gemm_fp8_block(q_x, s_x, q_w, s_w)
+    ref, err = product(q_x, s_x, q_w, s_w)
+    check_rounded(y, ref, err, 2.0 ** -8)
+
+
+@pytest.mark.parametrize("M,K,N", [(5, 256, 136), (70, 272, 200), (300, 528, 392)])
+def test_outputs_stay_inside_their_tensors(M, K, N):
+    g = gen(M)
+    q_x, s_x = activations(g, M, K)
+    N16 = -(-N // 16) * 16
+    wg, wu = weights(g, N16, K), weights(g, N16, K)
+
+    def framed(shape, dtype):
+        n = 1
+        for d in shape:
+            n *= d
+        n *= torch.empty((), dtype=dtype).element_size()
+        buf = torch.full((n + 512,), 0x5a, dtype=torch.uint8, device="cuda")
+        return buf, buf[256:256 + n].view(dtype).view(shape)
+
+    y_buf, y = framed((M, N16), torch.bfloat16)
+    dfk.dfk_gemm_fp8_block(q_x, s_x, *wg, y=y)
+    h_buf, h = framed((M, N16), torch.bfloat16)
+    dfk.dfk_swiglu_gate_up_fp8_block(q_x, s_x, *wg, *wu, fp8_out=False, h=h)
+    q_buf, q = framed((M, N16), E4M3)
+    s_buf, s = framed((-(-N16 // 128), M), torch.float32)
+    dfk.dfk_swiglu_gate_up_fp8_block(q_x, s_x, *wg, *wu, q_h=q, s_h=s)
+    c_buf, c = framed((M, N16), E4M3)
+    t_buf, t = framed((-(-N16 // 128), M), torch.float32)
+    r_buf, r = framed((M, N16), torch.bfloat16)
+    dfk.dfk_quant_fp8_block(h, q=c, s=t)
+    dfk.dfk_add_rmsnorm_fp8_block(h, y, torch.ones_like(h[0]), 1e-5, residual_out=r, q=c, s=t)
+    torch.cuda.synchronize()
+    for b in (y_buf, h_buf, q_buf, s_buf, c_buf, t_buf, r_buf):
+        assert (b[:256] == 0x5a).all() and (b[-256:] == 0x5a).all()
+    assert torch.equal(y, dfk.dfk_gemm_fp8_block(q_x, s_x, *wg))
+
+
+@pytest.mark.parametrize("M", [3, 40, 130, 300])
+def test_a_token_that_is_nan_leaves_the_others(M):
+    g = gen(M)
+    x = rand_bf16(g, M, 512)
+    wg, wu, wd = weights(g, 384, 512), weights(g, 384, 512), weights(g, 512, 384)
+
+    def mlp(x):
+        q, s, _ = dfk.dfk_add_rmsnorm_fp8_block(x, None, torch.ones_like(x[0]), 1e-5)
+        q, s = dfk.dfk_swiglu_gate_up_fp8_block(q, s, *wg, *wu)
+        return dfk.dfk_gemm_fp8_block(q, s, *wd)
+
+    clean = mlp(x)
+    x[1, 77] = float("nan")
+    y = mlp(x)
+    assert torch.isnan(y[1].float()).all()
+    keep = torch.arange(M, device="cuda") != 1
+    assert torch.equal(y[keep], clean[keep])
+
+
+@pytest.mark.parametrize("M", [1, 16, 64, 100, 256, 700])
+def test_same_bits_every_time(M):
+    g = gen(M)
+    q_x, s_x = activations(g, M, 2048)
+    wg, wu = weights(g, 1024, 2048), weights(g, 1024, 2048)
+    first = dfk.dfk_swiglu_gate_up_fp8_block(q_x, s_x, *wg, *wu)
+    y0 = dfk.dfk_gemm_fp8_block(q_x, s_x, *wg)
+    for _ in range(5):
+        q, s = dfk.dfk_swiglu_gate_up_fp8_block(q_x, s_x, *wg, *wu)
+        assert torch.equal(q.view(torch.uint8), first[0].view(torch.uint8))
+        assert torch.equal(s, first[1])
+        assert torch.equal(dfk.dfk_gemm_fp8_block(q_x, s_x, *wg), y0)
+
+
+# ---- together, as a model's layer runs them
+
+class Layer:
+    """x -> norm of x + residual -> gate/up -> down, every intermediate in 8 bits."""
+
+    def __init__(self, g, D, F):
+        self.gamma = (1 + 0.1 * torch.randn(D, generator=g, device="cuda")).bfloat16()
+        self.wg, self.wu, self.wd = weights(g, F, D), weights(g, F, D), weights(g, D, F)
+
+    def __call__(self, x, res, stream=None):
+        q, s, r = dfk.dfk_add_rmsnorm_fp8_block(x, res, self.gamma, 1e-5, stream=stream)
+        qh, sh = dfk.dfk_swiglu_gate_up_fp8_block(q, s, *self.wg, *self.wu, stream=stream)
+        return q, s, r, qh, sh, dfk.dfk_gemm_fp8_block(qh, sh, *self.wd, stream=stream)
+
+
+@pytest.mark.parametrize("M", [1, 7, 64, 150, 600])
+@pytest.mark.parametrize("D,F", [(256, 688), (1024, 3584)])
+def test_layer(M, D, F):
+    g = gen(M + D)
+    layer = Layer(g, D, F)
+    x, res = rand_bf16(g, M, D), rand_bf16(g, M, D)
+    q, s, r, qh, sh, y = layer(x, res)
+    d = r.double()
+    v = d / (d.square().mean(1, keepdim=True) + 1e-5).sqrt() * layer.gamma.double()
+    check_quantised(q, s, v, 2.0 ** -18 * v.abs())
+    h, eh = silu_mul(*product(q, s, *layer.wg), *product(q, s, *layer.wu))
+    check_quantised(qh, sh, h, eh)
+    ref, err = product(qh, sh, *layer.wd)
+    check_rounded(y, ref, err, 2.0 ** -8)
+
+
+def same(a, b):
+    return all(torch.equal(x.view(torch.uint8), y.view(torch.uint8)) for x, y in zip(a, b))
+
+
+@pytest.mark.parametrize("M", [1, 40, 300])
+def test_layer_in_a_graph_and_on_two_streams(M):
+    g = gen(M)
+    layers = [Layer(g, 512, 1024) for _ in range(2)]
+    xs = [(rand_bf16(g, M, 512), rand_bf16(g, M, 512)) for _ in range(2)]
+    want = [l(*x) for l, x in zip(layers, xs)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for _ in range(10):          # both streams at once
+        got = [l(*x, stream=st) for l, x, st in zip(layers, xs, streams)]
+        torch.cuda.synchronize()
+        assert all(same(a, b) for a, b in zip(got, want))
+    graphs, outs = [], []
+    for l, x, st in zip(layers, xs, streams):
+        gr = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(gr, stream=st):
+            outs.append(l(*x))
+        graphs.append(gr)
+    for _ in range(5):           # two captured graphs in flight at the same time
+        for o in outs:
+            for t in o:
+                t.view(torch.uint8).fill_(7)
+        torch.cuda.synchronize()
+        for gr, st in zip(graphs, streams):
+            with torch.cuda.stream(st):
+                gr.replay()
+        torch.cuda.synchronize()
+        assert all(same(a, b) for a, b in zip(outs, want))
+    for x, _ in xs:              # new inputs in the same buffers
+        x.copy_(rand_bf16(g, M, 512))
+    for gr in graphs:
+        gr.replay()
+    torch.cuda.synchronize()
+    assert all(same(o, l(*x)) for o, l, x in zip(outs, layers, xs))
+
+
+def test_large_offsets():
+    """Outputs whose offsets pass 32 bits: 70,000 tokens x 32,000 columns of bf16 (4.5 GB)."""
+    M, K, N = 70000, 128, 32000
+    g = gen(1)
+    q_x, s_x = activations(g, M, K)
+    q_w, s_w = weights(g, N, K)
+    y = dfk.dfk_gemm_fp8_block(q_x, s_x, q_w, s_w)
+    for lo in (0, 33554, 67100, M - 64):
+        a, b = q_x[lo:lo + 64].contiguous(), s_x[:, lo:lo + 64].contiguous()
+        ref, err = product(a, b, q_w, s_w)
+        check_rounded(y[lo:lo + 64], ref, err, 2.0 ** -8)
+
+
+def test_no_tokens():
+    e = torch.empty(0, 256, device="cuda", dtype=torch.bfloat16)
+    q, s = dfk.dfk_quant_fp8_block(e)
+    assert q.shape == (0, 256) and s.shape == (2, 0)
+    w = weights(gen(0), 64, 256)
+    assert dfk.dfk_gemm_fp8_block(q, s, *w).shape == (0, 64)
+    assert dfk.dfk_swiglu_gate_up_fp8_block(q, s, *w, *w)[0].shape == (0, 64)
+
+
+def test_binding_refusals():
+    g = gen(0)
+    q, s = activations(g, 4, 256)
+    qw, sw = weights(g, 128, 256)
+    ok = dfk.dfk_gemm_fp8_block(q, s, qw, sw)
+    for args, kw in (((q, s.t(), qw, sw), {}), ((q, s, qw.t(), sw), {}),
+                     ((q, s, qw, sw[:, :1]), {}), ((q.float(), s, qw, sw), {}),
+                     ((q, s.double(), qw, sw), {}), ((q, s, qw, sw), {"y": ok[:3]}),
+                     ((q, s, qw, sw), {"y": ok.float()}), ((q[0], s, qw, sw), {}),
+                     ((q, s, qw, sw.cpu()), {}), ((q, s, None, sw), {})):
+        with pytest.raises(dfk.DfkError) as e:
+            dfk.dfk_gemm_fp8_block(*args, **kw)
+        assert e.value.status == dfk.DFK_ERR_INVALID_ARG
+    x = torch.zeros(4, 200, device="cuda", dtype=torch.bfloat16)
+    with pytest.raises(dfk.DfkError) as e:
+        dfk.dfk_quant_fp8_block(x)            # 200 % 16
+    assert e.value.status == dfk.DFK_ERR_UNSUPPORTED_SHAPE
+    with pytest.raises(dfk.DfkError):
+        dfk.dfk_quant_fp8_block(torch.zeros(8, 64, device="cuda", dtype=torch.bfloat16).t())
+    with pytest.raises(dfk.DfkError):
+        dfk.dfk_swiglu_gate_up_fp8_block(q, s, qw, sw, qw, sw, h=ok)
+    with pytest.raises(dfk.DfkError):
+        dfk.dfk_swiglu_gate_up_fp8_block(q, s, qw, sw, qw, sw, fp8_out=False, q_h=q)
+
+
+CHILD = r'''
+import os, sys
+sys.path.insert(0, os.environ["DFK_ROOT"])
+sys.path.insert(0, os.path.join(os.environ["DFK_ROOT"], "tests"))
+import swiglu_mlp_dfk_b200 as dfk
+assert dfk.LIB_PATH.endswith("libdfk_checked.so")
+import test_gpu_fp8_block as t
+for M, K in ((1, 16), (5, 2064), (130, 256)):
+    t.test_quant(M, K)
+for M, D in ((3, 688), (2, 16400)):
+    t.test_add_rmsnorm(M, D, True)
+for M, K, N in ((1, 16, 1), (3, 2064, 1001), (33, 272, 96), (129, 1152, 640), (257, 384, 520)):
+    t.test_gemm(M, K, N)
+    t.test_gate_up(M, K, N, True)
+    t.test_gate_up(M, K, N, False)
+st = dfk.dfk_device_status()
+assert st[0] == 0, st
+print("checked ok")
+'''
+
+
+def test_checked_build():
+    env = dict(os.environ, DFK_CHECKED="1", DFK_ROOT=ROOT)
+    r = subprocess.run([sys.executable, "-c", CHILD], env=env, capture_output=True, text=True,
+                       timeout=600)
+    assert r.returncode == 0 and "checked ok" in r.stdout, r.stdout + r.stderr
