@@ -24,6 +24,9 @@ static int check_rows(int M, int K) {
 constexpr int FB_SMEM_MAX = 232448;     // bytes a CTA may use
 constexpr int FB_SMEM_HALF = 115712;    // two CTAs on an SM
 
+// Up to this many tokens a product streams its weights (fp8_block_small.cu).
+constexpr int FB_SMALL_MAX_M = 64;
+
 struct FbCall {
   int nmat;
   const void *qx;
@@ -68,6 +71,23 @@ static int launch_small(const FbCall &c, int sms, unsigned *err, cudaStream_t st
   return DFK_OK;
 }
 
+static int launch_large(const FbCall &c, int sms, unsigned *err, cudaStream_t st) {
+  const bool gate = c.nmat == 2;
+  int rc = api_allow_smem(fb_large_kernel_fn(gate));
+  if (rc) return rc;
+  FbMaps maps;
+  memset(&maps, 0, sizeof maps);
+  if ((rc = api_tensor_map_u8(c.qx, c.K, c.M, c.K, 128, 128, &maps.x))) return rc;
+  for (int m = 0; m < c.nmat; ++m)
+    if ((rc = api_tensor_map_u8(c.qw[m], c.K, c.N, c.K, 128, 128, &maps.w[m]))) return rc;
+  const FbParams p{c.sx, {c.sw[0], c.sw[1]}, static_cast<uint16_t *>(c.y),
+                   static_cast<uint8_t *>(c.qh), c.sh, err, c.M, c.N,
+                   (c.K + FB_GROUP - 1) / FB_GROUP, 0};
+  const cudaError_t e = launch_fb_large(gate, maps, p, sms, st, api_pdl());
+  if (e != cudaSuccess) return api_cuda_error(e, "block-scaled FP8 product launch");
+  return DFK_OK;
+}
+
 static int product(const FbCall &c, cudaStream_t st) {
   int rc = check_rows(c.M, c.K);
   if (rc) return rc;
@@ -95,7 +115,7 @@ static int product(const FbCall &c, cudaStream_t st) {
   int sms;
   unsigned *err;
   if ((rc = api_device(&sms, &err))) return rc;
-  return launch_small(c, sms, err, st);
+  return c.M <= FB_SMALL_MAX_M ? launch_small(c, sms, err, st) : launch_large(c, sms, err, st);
 }
 
 }  // namespace dfk

@@ -1,0 +1,549 @@
+// fp8_block_large.cu -- block-scaled FP8 products for many tokens (prompts):
+// bound by the E4M3 tensor-core MMA.
+//
+// A pair of CTAs (cluster of 2, cta_group::2) owns a tile of 256 tokens (the
+// MMA's M, 128 in each CTA's TMEM lanes) x 256 weight rows (its N; each CTA
+// brings 128 of them): 32 KB of codes per CTA and group of 128 feed 512
+// tensor-core cycles.  For the gated product CTA 0 brings 128 gate rows and
+// CTA 1 the matching 128 up rows, so each CTA holds both halves of 128
+// columns of h, which is one group of the quantised output.
+//
+// The scales change with every group, so a group's sums are taken out of TMEM
+// (two buffers of 256 columns: the tensor core fills one while the other is
+// read), multiplied by s_x s_w and added to fp32 registers: 128 sums in each
+// of 256 epilogue threads, one token per thread.  That costs 128 x 256 FMAs and
+// as many TMEM reads per group and CTA, 256 cycles of each pipe against the
+// MMA's 512.
+//
+// One persistent pair per two SMs walks the tiles in bands of FBL_BAND token
+// tiles, so that the tiles in flight share operands in L2.
+#include <algorithm>
+
+#include "fp8_block.cuh"
+#include "launch_util.h"
+#include "tc_ptx.cuh"
+#include "tf8mma_engine.cuh"
+
+namespace dfk {
+
+constexpr int FBL_THREADS = 384;   // TMA, MMA and two scale warps; eight epilogue warps
+// Registers a thread: 384 x 168 at launch, then 40 for the first warpgroup and
+// 232 for the two epilogue warpgroups (40 + 2 x 232 = 3 x 168).
+constexpr int FBL_REGS_IO = 40, FBL_REGS_EPI = 232;
+constexpr int FBL_STAGES = 6;
+constexpr int FBL_HALF = 128 * 128;           // bytes of one operand's half tile
+constexpr int FBL_STAGE = 2 * FBL_HALF;
+constexpr int FBL_AHEAD = 8;       // groups whose scales are on the way (a power of two)
+constexpr int FBL_COMB = 4;        // groups whose s_x s_w are ready (a power of two)
+constexpr int FBL_BAND = 8;
+
+constexpr int FBL_OFF_OUT = FBL_STAGES * FBL_STAGE;        // 8 warps x 2 KB: output rows
+constexpr int FBL_OFF_SX = FBL_OFF_OUT + 8 * 2048;         // [AHEAD][128] s_x
+constexpr int FBL_OFF_SW = FBL_OFF_SX + FBL_AHEAD * 512;   // [AHEAD][2 warps][2] s_w
+constexpr int FBL_OFF_COMB = FBL_OFF_SW + FBL_AHEAD * 16;  // [COMB][2][128] s_x s_w
+constexpr int FBL_OFF_MAX = FBL_OFF_COMB + FBL_COMB * 1024;  // [2 tiles][2][128] row maxima
+constexpr int FBL_OFF_BAR = FBL_OFF_MAX + 2048;
+constexpr int FBL_BARS = 2 * FBL_STAGES + 9;
+constexpr int FBL_SMEM = 1024 + FBL_OFF_BAR + FBL_BARS * 8 + 16;
+
+// ---- cta_group::2 forms
+
+__device__ __forceinline__ void tmem_alloc_pair(uint32_t *slot, uint32_t ncols) {
+  asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                   smem_addr(slot)),
+               "r"(ncols)
+               : "memory");
+}
+__device__ __forceinline__ void tmem_relinquish_pair() {
+  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tmem_dealloc_pair(uint32_t taddr, uint32_t ncols) {
+  asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols)
+               : "memory");
+}
+
+// D (both CTAs' TMEM) (+)= A B^T; the descriptors' offsets hold in both CTAs.
+__device__ __forceinline__ void umma_e4m3_pair(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
+                                               uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+// Arrive on the barrier at this offset in both CTAs once the MMAs issued so
+// far have completed.
+__device__ __forceinline__ void umma_commit_pair(uint64_t *bar) {
+  asm volatile(
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 "
+      "[%0], %1;" ::"r"(smem_addr(bar)),
+      "h"(static_cast<uint16_t>(3))
+      : "memory");
+}
+
+// Tile copy into this CTA's shared memory, counted on a barrier of the pair
+// (`bar`: a shared::cluster address, the leader's).
+__device__ __forceinline__ void tma_load_2d_pair(void *dst, const CUtensorMap *map, uint32_t bar,
+                                                 int c0, int c1, uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      ".cta_group::2.L2::cache_hint [%0], [%1, {%3, %4}], [%2], %5;" ::"r"(smem_addr(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(c1), "l"(policy)
+      : "memory");
+}
+
+// Arrive on a barrier of the pair (a shared::cluster address).  Release at CTA
+// scope: what it hands over are TMEM reads, ordered by tcgen05.wait::ld and
+// the fence before it.  A release at cluster scope waits for the thread's
+// global copies in flight: 1500 cycles per group.
+__device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar) {
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar)
+               : "memory");
+}
+
+// 32 TMEM columns of this warp's lanes; the values may be used after
+// tmem_wait32, which takes them as operands.
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
+      "%11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, "
+      "%28, %29, %30, %31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]),
+        "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]),
+        "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]),
+        "=r"(r[31])
+      : "r"(taddr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_wait32(uint32_t (&r)[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]),
+                 "+r"(r[6]), "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]),
+                 "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]), "+r"(r[16]), "+r"(r[17]),
+                 "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]),
+                 "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27])
+               :
+               : "memory");
+  asm volatile("" : "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31])::"memory");
+}
+
+__device__ __forceinline__ void cp_async4(uint32_t dst, const float *src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() {
+  asm volatile("cp.async.commit_group;" ::: "memory");
+}
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// Tile number -> (token tile, column tile): bands of FBL_BAND token tiles,
+// inside a band column tile by column tile.
+struct FblTiles {
+  int tm, tn;
+  __device__ __forceinline__ int count() const { return tm * tn; }
+  __device__ __forceinline__ void at(int t, int &m, int &n) const {
+    const int band = t / (FBL_BAND * tn), r = t - band * FBL_BAND * tn;
+    const int h = min(FBL_BAND, tm - band * FBL_BAND);
+    n = r / h;
+    m = band * FBL_BAND + (r - n * h);
+  }
+};
+
+// 64 bytes of each of the warp's 32 rows (lane = row) to global memory, whole
+// 32-byte sectors a row: through 2 KB of shared memory, chunks of 16 bytes
+// swizzled so that neither side meets a bank twice.
+template <typename Store>
+__device__ __forceinline__ void fbl_rows64(uint8_t *buf, int lane, const uint32_t (&w)[16],
+                                           Store store) {
+#pragma unroll
+  for (int c = 0; c < 4; ++c)
+    *reinterpret_cast<uint4 *>(buf + lane * 64 + ((c ^ ((lane >> 1) & 3)) << 4)) =
+        make_uint4(w[4 * c], w[4 * c + 1], w[4 * c + 2], w[4 * c + 3]);
+  __syncwarp();
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int r = 8 * i + (lane >> 2), c = lane & 3;
+    store(r, c, *reinterpret_cast<const uint4 *>(buf + r * 64 + ((c ^ ((r >> 1) & 3)) << 4)));
+  }
+  __syncwarp();
+}
+
+// Eight bf16 of row m, columns col .. col + 7.
+__device__ __forceinline__ void fbl_store_bf16(const FbParams &p, int m, int col, const uint4 &v) {
+  if (m >= p.M || col >= p.N) return;
+  uint16_t *at = p.y + static_cast<size_t>(m) * p.N + col;
+  if ((p.N & 7) == 0) {
+    if (DFK_IN_BOUNDS(col + 8 <= p.N, 31, p.err)) *reinterpret_cast<uint4 *>(at) = v;
+    return;
+  }
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int e = 0; e < 8; ++e)
+    if (col + e < p.N) at[e] = static_cast<uint16_t>(w[e >> 1] >> (16 * (e & 1)));
+}
+
+__device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
+  return f32_to_bf16_bits(lo) | (static_cast<uint32_t>(f32_to_bf16_bits(hi)) << 16);
+}
+
+template <bool GATE>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(FBL_THREADS, 1)
+    fb_large_kernel(const __grid_constant__ FbMaps maps, const FbParams p) {
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  const uint32_t raw_addr = smem_addr(smem_raw);
+  uint8_t *smem = smem_raw + ((1024u - (raw_addr & 1023u)) & 1023u);
+  const uint32_t sbase = smem_addr(smem);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  constexpr int S = FBL_STAGES;
+
+  uint64_t *fullb = reinterpret_cast<uint64_t *>(smem + FBL_OFF_BAR);  // the leader's count
+  uint64_t *empty = fullb + S;
+  uint64_t *accfull = empty + S;    // [2]
+  uint64_t *accempty = accfull + 2; // [2], the leader's count
+  uint64_t *maxfull = accempty + 2; // [4] row maxima of both halves written, per lane quarter
+  uint64_t *done = maxfull + 4;
+  volatile int *s_abort = reinterpret_cast<volatile int *>(done + 1);
+  int *s_issued = reinterpret_cast<int *>(done + 1) + 1;
+  uint32_t *s_tmem = reinterpret_cast<uint32_t *>(done + 1) + 2;
+
+  const uint32_t rank = cluster_rank();
+  const int pair = blockIdx.x >> 1, npairs = gridDim.x >> 1;
+  const int NB = (p.N + 127) / 128;  // scale blocks along the weight rows
+  const FblTiles tiles{(p.M + 255) / 256, GATE ? NB : (p.N + 255) / 256};
+  const int ntiles = tiles.count();
+
+  if (tid == 0) {
+    for (int s = 0; s < S; ++s) {
+      mbar_init(&fullb[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&accfull[s], 3);    // the MMAs of a group and both scale warps
+      mbar_init(&accempty[s], 16);  // eight epilogue warps of each CTA
+    }
+    for (int s = 0; s < 4; ++s) mbar_init(&maxfull[s], 2);
+    mbar_init(done, 1);
+    *s_abort = 0;
+    *s_issued = 0;
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    tmem_alloc_pair(s_tmem, 512);
+    tmem_relinquish_pair();
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync_all();  // both CTAs' barriers exist before either is signalled
+  tc_fence_after();
+  const uint32_t tmem = *s_tmem;
+  pdl_launch_dependents();
+
+  if (warp < 4) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(FBL_REGS_IO));
+  if (warp == 0) {
+    // ---- TMA: this CTA's 128 tokens and its 128 weight rows of every group
+    if (lane == 0) {
+      const uint64_t pol = l2_policy_evict_normal();
+      pdl_wait();
+      int it = 0;
+      bool ok = true;
+      for (int t = pair; ok && t < ntiles; t += npairs) {
+        int tm, tn;
+        tiles.at(t, tm, tn);
+        const int mrow = tm * 256 + static_cast<int>(rank) * 128;
+        const int wrow = GATE ? tn * 128 : tn * 256 + static_cast<int>(rank) * 128;
+        const CUtensorMap *wmap = GATE && rank ? &maps.w[1] : &maps.w[0];
+        for (int kb = 0; kb < p.G; ++kb, ++it) {
+          const int st = it % S;
+          if (it >= S && !fb_wait(&empty[st], ((it / S) - 1) & 1, s_abort, p.err)) {
+            ok = false;
+            break;
+          }
+          if (rank == 0) mbar_arrive_expect_tx(&fullb[st], 2 * FBL_STAGE);
+          const uint32_t bar = cluster_map(smem_addr(&fullb[st]), 0);
+          uint8_t *sb = smem + st * FBL_STAGE;
+          tma_load_2d_pair(sb, &maps.x, bar, kb * 128, mrow, pol);
+          tma_load_2d_pair(sb + FBL_HALF, wmap, bar, kb * 128, wrow, pol);
+        }
+      }
+      *s_issued = it;
+      // the last stages' releases have arrived before this CTA may leave
+      for (int i = max(0, it - S); ok && i < it; ++i)
+        ok = fb_wait(&empty[i % S], (i / S) & 1, s_abort, p.err);
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    // ---- MMA, the leader CTA for both: 4 instructions of K = 32 per group
+    const uint32_t leader = elect_one_sync();
+    if (rank == 0) {
+      const uint32_t idesc = umma_idesc_e4m3_f32(256, 256);
+      const uint64_t desc0 = umma_desc_sw128(sbase);
+      int it = 0;
+      bool ok = true;
+      for (int t = pair; ok && t < ntiles; t += npairs) {
+        for (int kb = 0; kb < p.G; ++kb, ++it) {
+          const int st = it % S, ab = it & 1;
+          ok = fb_wait(&fullb[st], (it / S) & 1, s_abort, p.err);
+          if (ok && it >= 2)
+            ok = fb_wait(&accempty[ab], ((it >> 1) - 1) & 1, s_abort, p.err);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+          tc_fence_after();
+          const uint64_t da = desc0 + (static_cast<uint32_t>(st * FBL_STAGE) >> 4);
+          const uint64_t db = da + (FBL_HALF >> 4);
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk)
+            if (leader)
+              umma_e4m3_pair(tmem + static_cast<uint32_t>(ab * 256), da + 2 * kk, db + 2 * kk,
+                             idesc, kk > 0 ? 1u : 0u);
+          if (leader) {
+            umma_commit_pair(&empty[st]);
+            umma_commit_pair(&accfull[ab]);
+          }
+          __syncwarp();
+        }
+      }
+      if (leader) umma_commit_pair(done);
+      __syncwarp();
+    }
+  } else if (warp < 4) {
+    // ---- scales: the product s_x s_w of every token and both halves of the
+    // tile's columns (gated: both matrices), a few groups ahead of the epilogue.
+    // A warp takes 64 tokens; raw scales are copied FBL_AHEAD groups ahead.
+    const int w = warp - 2, row = 64 * w + lane;
+    float *s_sx = reinterpret_cast<float *>(smem + FBL_OFF_SX);
+    float *s_sw = reinterpret_cast<float *>(smem + FBL_OFF_SW) + 2 * w;
+    float *s_comb = reinterpret_cast<float *>(smem + FBL_OFF_COMB);
+    const uint32_t sx_at = smem_addr(s_sx + row), sw_at = smem_addr(s_sw + lane);
+    pdl_wait();  // s_x comes from the previous kernel
+    int ft = pair, fkb = 0, fn = 0;
+    const float *fx = nullptr, *fw = nullptr;
+    bool in0 = false, in1 = false, inw = false;
+    auto fetch_tile = [&]() {
+      int tm = 0, tn = 0;
+      if (ft < ntiles) tiles.at(ft, tm, tn);
+      const int m = tm * 256 + static_cast<int>(rank) * 128 + row;
+      in0 = ft < ntiles && m < p.M;
+      in1 = ft < ntiles && m + 32 < p.M;
+      fx = p.sx + (in0 ? m : 0);
+      inw = ft < ntiles && lane < 2;
+      const int nb = GATE ? tn : min(2 * tn + lane, NB - 1);
+      fw = (GATE && lane == 1 ? p.sw[1] : p.sw[0]) + (inw ? static_cast<size_t>(nb) * p.G : 0);
+    };
+    auto fetch = [&]() {
+      const uint32_t slot = static_cast<uint32_t>(fn & (FBL_AHEAD - 1));
+      const float *x = fx + static_cast<size_t>(fkb) * p.M;
+      if (in0 && DFK_IN_BOUNDS(fkb < p.G, 32, p.err)) cp_async4(sx_at + slot * 512, x);
+      if (in1) cp_async4(sx_at + slot * 512 + 128, x + 32);
+      if (inw) cp_async4(sw_at + slot * 16, fw + fkb);
+      cp_async_commit();
+      ++fn;
+      if (++fkb == p.G) {
+        fkb = 0;
+        ft += npairs;
+        fetch_tile();
+      }
+    };
+    fetch_tile();
+#pragma unroll 1
+    for (int i = 0; i < FBL_AHEAD - 1; ++i) fetch();
+    const int total = ((ntiles - pair + npairs - 1) / npairs) * p.G;
+#pragma unroll 1
+    for (int it = 0; it < total; ++it) {
+      const int slot = it & (FBL_AHEAD - 1), cs = it & (FBL_COMB - 1);
+      cp_async_wait<FBL_AHEAD - 2>();
+      __syncwarp();
+      const float x0 = s_sx[slot * 128 + row], x1 = s_sx[slot * 128 + row + 32];
+      const float w0 = s_sw[slot * 4], w1 = s_sw[slot * 4 + 1];
+      fetch();  // into the slot of the group before this one
+      // One barrier tells the epilogue that a group's sums and its scales are
+      // there.  Group it - 2 is complete before `it` arrives on the same
+      // barrier; its MMAs followed the epilogue's release of group it - 4, the
+      // last to use this slot.
+      const bool ok = it < 2 || fb_wait(&accfull[it & 1], ((it >> 1) - 1) & 1, s_abort, p.err);
+      if (!__all_sync(0xffffffffu, ok)) break;
+      float *c = s_comb + cs * 256 + row;
+      c[0] = x0 * w0;
+      c[32] = x1 * w0;
+      c[128] = x0 * w1;
+      c[160] = x1 * w1;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&accfull[it & 1]);
+    }
+    cp_async_wait<0>();
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(FBL_REGS_EPI));
+    // ---- epilogue: thread = one token (TMEM lane) and half of the columns
+    const int ew = warp - 4, half = ew >> 2, q = warp & 3;
+    const int row = 32 * q + lane;
+    const uint32_t base = tmem + (static_cast<uint32_t>(32 * q) << 16);
+    const float *s_comb = reinterpret_cast<const float *>(smem + FBL_OFF_COMB) + row;
+    float *s_max = reinterpret_cast<float *>(smem + FBL_OFF_MAX);
+    uint8_t *obuf = smem + FBL_OFF_OUT + ew * 2048;
+    const uint32_t empty_at[2] = {cluster_map(smem_addr(&accempty[0]), 0),
+                                  cluster_map(smem_addr(&accempty[1]), 0)};
+    pdl_wait();  // the outputs may still be read by the previous kernel
+
+    int it = 0, nth = 0;
+    bool ok = true;
+    for (int t = pair; ok && t < ntiles; t += npairs, ++nth) {
+      uint64_t acc[64];  // pairs of neighbouring columns
+#pragma unroll
+      for (int i = 0; i < 64; ++i) acc[i] = 0ull;
+      // A step waits for 32 columns, sends for the next 32 (past the end of a
+      // group: the next group's first, once it is complete) and adds the ones
+      // that are there, so a load is always on its way.
+      uint32_t d[2][32];
+      auto ready = [&]() {
+        ok = __all_sync(0xffffffffu, fb_wait(&accfull[it & 1], (it >> 1) & 1, s_abort, p.err));
+        tc_fence_after();
+        return ok;
+      };
+      const uint32_t tb = base + (GATE ? 64 : 128) * half;
+      if (!ready()) break;
+      tmem_ld32(tb + (it & 1) * 256, d[0]);
+#pragma unroll 1
+      for (int kb = 0;;) {
+        const int ab = it & 1, cs = it & (FBL_COMB - 1);
+        const float s0 = s_comb[cs * 256 + (GATE ? 0 : 128 * half)];
+        const float s1 = GATE ? s_comb[cs * 256 + 128] : s0;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          tmem_wait32(d[c & 1]);
+          if (c < 3) {
+            tmem_ld32(tb + ab * 256 + (GATE && c >= 1 ? 32 * (c + 1) + 64 : 32 * (c + 1)),
+                      d[(c + 1) & 1]);
+          } else {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_cluster(empty_at[ab]);
+            ++it;
+            if (++kb < p.G && ready()) tmem_ld32(tb + (it & 1) * 256, d[0]);
+          }
+          const uint64_t sc = c < 2 ? pack_f32x2(s0, s0) : pack_f32x2(s1, s1);
+#pragma unroll
+          for (int e = 0; e < 16; ++e)
+            acc[16 * c + e] = fma_f32x2(
+                pack_f32x2(__uint_as_float(d[c & 1][2 * e]), __uint_as_float(d[c & 1][2 * e + 1])),
+                sc, acc[16 * c + e]);
+        }
+        if (kb == p.G || !ok) break;
+      }
+      if (!ok) break;
+      // ---- the tile's output
+      int tm, tn;
+      tiles.at(t, tm, tn);
+      const int m0 = tm * 256 + static_cast<int>(rank) * 128 + 32 * q;  // the warp's first row
+      if constexpr (!GATE) {
+        const int n0 = tn * 256 + 128 * half;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          uint32_t w[16];
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            float lo, hi;
+            unpack_f32x2(acc[16 * c + e], lo, hi);
+            w[e] = pack_bf16x2(lo, hi);
+          }
+          fbl_rows64(obuf, lane, w, [&](int r, int cc, const uint4 &v) {
+            fbl_store_bf16(p, m0 + r, n0 + 32 * c + 8 * cc, v);
+          });
+        }
+      } else {
+        const int n0 = tn * 128 + 64 * half;
+        float h[64];
+#pragma unroll
+        for (int e = 0; e < 32; ++e) {
+          float g0, g1, u0, u1;
+          unpack_f32x2(acc[e], g0, g1);
+          unpack_f32x2(acc[32 + e], u0, u1);
+          h[2 * e] = fb_silu_mul(g0, u0);
+          h[2 * e + 1] = fb_silu_mul(g1, u1);
+        }
+        if (p.y != nullptr) {
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            uint32_t w[16];
+#pragma unroll
+            for (int e = 0; e < 16; ++e) w[e] = pack_bf16x2(h[32 * c + 2 * e], h[32 * c + 2 * e + 1]);
+            fbl_rows64(obuf, lane, w, [&](int r, int cc, const uint4 &v) {
+              fbl_store_bf16(p, m0 + r, n0 + 32 * c + 8 * cc, v);
+            });
+          }
+        } else {
+          // the group's other 64 columns are in the warp with the same rows
+          float mx = 0.f;
+#pragma unroll
+          for (int e = 0; e < 64; ++e)
+            if (n0 + e < p.N) mx = max_nan(mx, fabsf(h[e]));
+          // (two buffers: a warp that writes tile nth + 2 has seen the other
+          // one at tile nth + 1, after its read of nth)
+          float *mb = s_max + (nth & 1) * 256;
+          mb[half * 128 + row] = mx;
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&maxfull[q]);
+          ok = __all_sync(0xffffffffu, fb_wait(&maxfull[q], nth & 1, s_abort, p.err));
+          if (!ok) break;
+          mx = max_nan(mx, mb[(1 - half) * 128 + row]);
+          const FbScale f = fb_scale(mx);
+          uint32_t w[16];
+#pragma unroll
+          for (int e = 0; e < 16; ++e)
+            w[e] = fb_codes4(h[4 * e], h[4 * e + 1], h[4 * e + 2], h[4 * e + 3], f);
+          fbl_rows64(obuf, lane, w, [&](int r, int cc, const uint4 &v) {
+            const int m = m0 + r, col = n0 + 16 * cc;
+            if (m < p.M && col < p.N && DFK_IN_BOUNDS(col + 16 <= p.N, 33, p.err))
+              *reinterpret_cast<uint4 *>(p.qh + static_cast<size_t>(m) * p.N + col) = v;
+          });
+          if (half == 0 && m0 + lane < p.M && DFK_IN_BOUNDS(tn < NB, 34, p.err))
+            p.sh[static_cast<size_t>(tn) * p.M + m0 + lane] = f.s;
+        }
+      }
+    }
+  }
+
+  // every wait above is bounded, so both CTAs come here; the MMAs have
+  // completed and both CTAs' copies have landed before either leaves
+  __syncthreads();
+  if (tid == 0) {
+    fb_wait(done, 0, nullptr, p.err);
+    if (*s_abort) {
+      const int issued = *s_issued;
+      if (rank == 0)
+        for (int i = max(0, issued - S); i < issued; ++i)
+          fb_wait(&fullb[i % S], (i / S) & 1, nullptr, p.err);
+      // copies that only one of the CTAs issued are counted by no complete
+      // phase: they land within microseconds, allow a millisecond
+      const unsigned long long t0 = global_timer_ns();
+      for (int i = 0; i < 100000 && global_timer_ns() - t0 < 1000000ull; ++i) __nanosleep(1000);
+    }
+  }
+  __syncthreads();
+  cluster_sync_all();
+  tc_fence_after();
+  if (warp == 1) tmem_dealloc_pair(tmem, 512);
+}
+
+cudaError_t launch_fb_large(bool gate, const FbMaps &maps, const FbParams &p, int sms,
+                            cudaStream_t st, bool pdl) {
+  const void *fn = fb_large_kernel_fn(gate);
+  const long long tm = (p.M + 255) / 256, tn = gate ? (p.N + 127) / 128 : (p.N + 255) / 256;
+  const long long pairs = std::min<long long>(sms / 2, tm * tn);
+  FbMaps mp = maps;
+  FbParams pp = p;
+  void *args[] = {&mp, &pp};
+  return launch_kernel(fn, dim3(static_cast<unsigned>(2 * pairs)), dim3(FBL_THREADS), FBL_SMEM,
+                       st, pdl, args);
+}
+
+const void *fb_large_kernel_fn(bool gate) {
+  return gate ? reinterpret_cast<const void *>(&fb_large_kernel<true>)
+              : reinterpret_cast<const void *>(&fb_large_kernel<false>);
+}
+
+}  // namespace dfk

@@ -109,7 +109,7 @@ __global__ void __launch_bounds__(FBS_THREADS)
       for (int i = 0; i < S0; ++i) load_x(i);
       int issued = S0;
       for (int i = S0; i < nkb; ++i) {
-        if (!mbar_wait_bounded(&empty[i % S], ((i / S) - 1) & 1, s_abort, p.err)) break;
+        if (!fb_wait(&empty[i % S], ((i / S) - 1) & 1, s_abort, p.err)) break;
         load_w(i);
         load_x(i);
         issued = i + 1;
@@ -124,8 +124,8 @@ __global__ void __launch_bounds__(FBS_THREADS)
     const uint64_t desc0 = umma_desc_sw128(sbase);
     for (int i = 0; i < nkb; ++i) {
       const int st = i % S, ab = i & 1;
-      bool ok = mbar_wait_bounded(&fullb[st], (i / S) & 1, s_abort, p.err);
-      if (ok && i >= 2) ok = mbar_wait_bounded(&accempty[ab], ((i >> 1) - 1) & 1, s_abort, p.err);
+      bool ok = fb_wait(&fullb[st], (i / S) & 1, s_abort, p.err);
+      if (ok && i >= 2) ok = fb_wait(&accempty[ab], ((i >> 1) - 1) & 1, s_abort, p.err);
       if (!__all_sync(0xffffffffu, ok)) break;
       tc_fence_after();
       const uint64_t ds = desc0 + (static_cast<uint32_t>(st * Sh::stage_bytes) >> 4);
@@ -190,7 +190,7 @@ __global__ void __launch_bounds__(FBS_THREADS)
               if (BN >= 32 || lane < BN) cb[m * BN + lane + 32 * e] = psx[u][e] * psw[u][m];
           fetch(i + FBS_PRE, psx[u], psw[u]);
           __syncwarp();
-          go = __all_sync(0xffffffffu, mbar_wait_bounded(&accfull[ab], (i >> 1) & 1, s_abort,
+          go = __all_sync(0xffffffffu, fb_wait(&accfull[ab], (i >> 1) & 1, s_abort,
                                                          p.err));
           if (go) {
             tc_fence_after();
@@ -231,7 +231,7 @@ __global__ void __launch_bounds__(FBS_THREADS)
   // cluster meets (after an abort; normally all have been consumed)
   __syncthreads();
   if (warp == 1) {
-    if (lane == 0) mbar_wait_bounded(done, 0, nullptr, p.err);
+    if (lane == 0) fb_wait(done, 0, nullptr, p.err);
     __syncwarp();
     tc_fence_after();
     tmem_dealloc(tmem, Sh::tmem_cols);
@@ -242,7 +242,7 @@ __global__ void __launch_bounds__(FBS_THREADS)
       int last = -1;
       for (int i = issued - 1; i >= 0 && i >= issued - S; --i)
         if (i % S == st) { last = i; break; }
-      if (last >= 0) mbar_wait_bounded(&fullb[st], (last / S) & 1, nullptr, p.err);
+      if (last >= 0) fb_wait(&fullb[st], (last / S) & 1, nullptr, p.err);
     }
   }
   __syncwarp();
