@@ -359,54 +359,74 @@ def dfk_rmsnorm_qkv_proj(x, gamma, eps, w_qkv, n_q, n_k, n_v, q=None, k=None, v=
 
 # ---- block-scaled FP8: any number of tokens, 8-bit activations
 
-_FP8_CODES = (torch.float8_e4m3fn, torch.uint8)
+_E4M3 = torch.float8_e4m3fn
+_FP8_CODES = (_E4M3, torch.uint8)
+_BF16_ONLY = (_BF16,)
+_F32_ONLY = (torch.float32,)
+_Tensor = torch.Tensor
+_get_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 
-def _fb_check(name, t, dtypes, shape, device):
-    if not (isinstance(t, torch.Tensor) and t.is_cuda and t.dtype in dtypes):
-        raise DfkError(DFK_ERR_INVALID_ARG, "%s must be a CUDA tensor of %s"
-                       % (name, " or ".join(str(d)[6:] for d in dtypes)))
-    if tuple(t.shape) != shape or not t.is_contiguous():
-        raise DfkError(DFK_ERR_INVALID_ARG, "%s must be contiguous, of shape %s" % (name, shape))
-    if t.device != device:
-        raise DfkError(DFK_ERR_INVALID_ARG, "%s is on %s, not on %s" % (name, t.device, device))
+def _fb_refuse(name, t, dtypes, shape, dev):
+    if not isinstance(t, _Tensor) or not t.is_cuda or t.dtype not in dtypes:
+        why = "must be a CUDA tensor of " + " or ".join(str(d)[6:] for d in dtypes)
+    elif tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+        why = "must be contiguous, of shape %s" % (tuple(shape),)
+    else:
+        why = "is on cuda:%d, not on cuda:%d" % (t.get_device(), dev)
+    raise DfkError(DFK_ERR_INVALID_ARG, "%s %s" % (name, why))
+
+
+# Up to seven of these a call: a few attribute reads each (0.4 us).
+def _fb_check(name, t, dtypes, shape, dev):
+    if not (isinstance(t, _Tensor) and t.dtype in dtypes and t.shape == shape
+            and t.get_device() == dev and t.is_contiguous()):
+        _fb_refuse(name, t, dtypes, shape, dev)
 
 
 def _fb_rows(name, t):
-    """The [M, K] tensor that the other arguments' sizes and device go by."""
-    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dim() != 2:
+    """(rows, columns, device index) of the tensor the other arguments are measured by."""
+    if not isinstance(t, _Tensor) or t.dim() != 2 or not t.is_cuda:
         raise DfkError(DFK_ERR_INVALID_ARG, "%s must be a 2-D CUDA tensor" % name)
-    return t.shape[0], t.shape[1], t.device
+    shape = t.shape
+    return shape[0], shape[1], t.get_device()
 
 
-def _fb_call(device, stream, fn, *args):
-    """fn(*args, stream) with `device` current: the call's own stream is the given one, or the
-    current one of that device."""
-    if device.index == torch.cuda.current_device():
-        _check(fn(*args, _stream(stream)))
+def _fb_call(dev, stream, fn, *args):
+    """fn(*args, stream) with device `dev` current; stream None: that device's current one."""
+    if dev == _get_device():
+        if stream is None and _raw_stream is not None:
+            status = fn(*args, _raw_stream(dev))
+        else:
+            status = fn(*args, _stream(stream))
+        if status:
+            _check(status)
     else:
-        with torch.cuda.device(device):
+        with torch.cuda.device(dev):
             _check(fn(*args, _stream(stream)))
 
 
-def _fb_out(shape, dtype, device, stream):
-    """An output the caller did not give, allocated for the stream that writes it."""
-    t = torch.empty(shape, dtype=dtype, device=device)
-    if stream is not None and t.numel():
+def _fb_keep(t, stream):
+    """An output allocated here and written on a given stream is kept for that stream."""
+    if t.numel():
         t.record_stream(stream if hasattr(stream, "cuda_stream")
-                        else torch.cuda.ExternalStream(int(stream), device=device))
-    return t
+                        else torch.cuda.ExternalStream(int(stream), device=t.device))
 
 
-def _fb_codes_out(q, s, M, K, device, stream):
+def _fb_codes_out(q, s, M, K, dev, stream, like):
+    G = (K + 127) // 128
     if q is None:
-        q = _fb_out((M, K), torch.float8_e4m3fn, device, stream)
+        q = torch.empty(M, K, dtype=_E4M3, device=like.device)  # separate sizes: 1 us less
+        if stream is not None:
+            _fb_keep(q, stream)
     else:
-        _fb_check("q", q, _FP8_CODES, (M, K), device)
+        _fb_check("q", q, _FP8_CODES, (M, K), dev)
     if s is None:
-        s = _fb_out((-(-K // 128), M), torch.float32, device, stream)
+        s = torch.empty(G, M, dtype=torch.float32, device=like.device)
+        if stream is not None:
+            _fb_keep(s, stream)
     else:
-        _fb_check("s", s, (torch.float32,), (-(-K // 128), M), device)
+        _fb_check("s", s, _F32_ONLY, (G, M), dev)
     return q, s
 
 
@@ -414,9 +434,10 @@ def dfk_quant_fp8_block(x, q=None, s=None, stream=None):
     """Block-scaled FP8 of x [M, K] bf16: returns (q [M, K] float8_e4m3fn, s [ceil(K/128), M]
     fp32), s = max(max|x| / 448, 2^-126) per token and group of 128, q = E4M3(x / s)."""
     M, K, dev = _fb_rows("x", x)
-    _fb_check("x", x, (_BF16,), (M, K), dev)
-    q, s = _fb_codes_out(q, s, M, K, dev, stream)
-    _fb_call(dev, stream, lib().dfk_quant_fp8_block, _ptr(x), _ptr(q), _ptr(s), M, K)
+    _fb_check("x", x, _BF16_ONLY, (M, K), dev)
+    q, s = _fb_codes_out(q, s, M, K, dev, stream, x)
+    _fb_call(dev, stream, lib().dfk_quant_fp8_block, x.data_ptr(), q.data_ptr(), s.data_ptr(), M,
+             K)
     return q, s
 
 
@@ -426,43 +447,46 @@ def dfk_add_rmsnorm_fp8_block(x, residual, gamma, eps, residual_out=None, q=None
     RMSNorm(r; gamma, eps): returns (q, s, r), r None without a residual.  residual_out may be
     `residual` or `x` itself: the sum is then kept in place."""
     M, D, dev = _fb_rows("x", x)
-    _fb_check("x", x, (_BF16,), (M, D), dev)
-    _fb_check("gamma", gamma, (_BF16,), (D,), dev)
+    _fb_check("x", x, _BF16_ONLY, (M, D), dev)
+    _fb_check("gamma", gamma, _BF16_ONLY, (D,), dev)
     if residual is not None:
-        _fb_check("residual", residual, (_BF16,), (M, D), dev)
+        _fb_check("residual", residual, _BF16_ONLY, (M, D), dev)
         if residual_out is None:
-            residual_out = _fb_out((M, D), _BF16, dev, stream)
+            residual_out = torch.empty_like(residual)
+            if stream is not None:
+                _fb_keep(residual_out, stream)
     if residual_out is not None:
-        _fb_check("residual_out", residual_out, (_BF16,), (M, D), dev)
-    q, s = _fb_codes_out(q, s, M, D, dev, stream)
-    _fb_call(dev, stream, lib().dfk_add_rmsnorm_fp8_block, _ptr(x), _ptr(residual), _ptr(gamma),
-             float(eps), _ptr(residual_out), _ptr(q), _ptr(s), M, D)
+        _fb_check("residual_out", residual_out, _BF16_ONLY, (M, D), dev)
+    q, s = _fb_codes_out(q, s, M, D, dev, stream, x)
+    _fb_call(dev, stream, lib().dfk_add_rmsnorm_fp8_block, x.data_ptr(), _ptr(residual),
+             gamma.data_ptr(), float(eps), _ptr(residual_out), q.data_ptr(), s.data_ptr(), M, D)
     return q, s, residual_out
 
 
-def _fb_operands(q_x, s_x, weights):
+def _fb_operands(q_x, s_x, q_w, s_w, name):
     M, K, dev = _fb_rows("q_x", q_x)
-    G = -(-K // 128)
+    N = _fb_rows(name, q_w)[0]
+    G = (K + 127) // 128
     _fb_check("q_x", q_x, _FP8_CODES, (M, K), dev)
-    _fb_check("s_x", s_x, (torch.float32,), (G, M), dev)
-    N = _fb_rows(*weights[0][:2])[0]
-    for name, q, s in weights:
-        _fb_check(name, q, _FP8_CODES, (N, K), dev)
-        _fb_check("s" + name[1:], s, (torch.float32,), (-(-N // 128), G), dev)
-    return M, K, N, dev
+    _fb_check("s_x", s_x, _F32_ONLY, (G, M), dev)
+    _fb_check(name, q_w, _FP8_CODES, (N, K), dev)
+    _fb_check("s" + name[1:], s_w, _F32_ONLY, ((N + 127) // 128, G), dev)
+    return M, K, N, G, dev
 
 
 def dfk_gemm_fp8_block(q_x, s_x, q_w, s_w, y=None, stream=None):
     """y = x W^T, x in block-scaled FP8 (q_x [M, K], s_x [ceil(K/128), M]), W as E4M3 codes
     q_w [N, K] with one fp32 scale per 128 x 128 block, s_w [ceil(N/128), ceil(K/128)];
     returns y [M, N] bf16."""
-    M, K, N, dev = _fb_operands(q_x, s_x, (("q_w", q_w, s_w),))
+    M, K, N, _, dev = _fb_operands(q_x, s_x, q_w, s_w, "q_w")
     if y is None:
-        y = _fb_out((M, N), _BF16, dev, stream)
+        y = torch.empty(M, N, dtype=_BF16, device=s_x.device)
+        if stream is not None:
+            _fb_keep(y, stream)
     else:
-        _fb_check("y", y, (_BF16,), (M, N), dev)
-    _fb_call(dev, stream, lib().dfk_gemm_fp8_block, _ptr(q_x), _ptr(s_x), _ptr(q_w), _ptr(s_w),
-             _ptr(y), M, K, N)
+        _fb_check("y", y, _BF16_ONLY, (M, N), dev)
+    _fb_call(dev, stream, lib().dfk_gemm_fp8_block, q_x.data_ptr(), s_x.data_ptr(),
+             q_w.data_ptr(), s_w.data_ptr(), y.data_ptr(), M, K, N)
     return y
 
 
@@ -471,20 +495,27 @@ def dfk_swiglu_gate_up_fp8_block(q_x, s_x, q_gate, s_gate, q_up, s_up, fp8_out=T
     """h = SiLU(x W_gate^T) * (x W_up^T) in one kernel, operands as for dfk_gemm_fp8_block
     (W_gate, W_up [d_ff, d_model]).  fp8_out: returns (q_h, s_h), h in block-scaled FP8 from its
     fp32 values; otherwise returns h [M, d_ff] bf16."""
-    M, D, F, dev = _fb_operands(q_x, s_x, (("q_gate", q_gate, s_gate), ("q_up", q_up, s_up)))
+    M, D, F, G, dev = _fb_operands(q_x, s_x, q_gate, s_gate, "q_gate")
+    _fb_check("q_up", q_up, _FP8_CODES, (F, D), dev)
+    _fb_check("s_up", s_up, _F32_ONLY, ((F + 127) // 128, G), dev)
     if fp8_out:
         if h is not None:
             raise DfkError(DFK_ERR_INVALID_ARG, "h is the bf16 output: fp8_out=False")
-        q_h, s_h = _fb_codes_out(q_h, s_h, M, F, dev, stream)
+        q_h, s_h = _fb_codes_out(q_h, s_h, M, F, dev, stream, s_x)
+        ph, pq, ps = None, q_h.data_ptr(), s_h.data_ptr()
     else:
         if q_h is not None or s_h is not None:
             raise DfkError(DFK_ERR_INVALID_ARG, "q_h and s_h are the FP8 output: fp8_out=True")
         if h is None:
-            h = _fb_out((M, F), _BF16, dev, stream)
+            h = torch.empty(M, F, dtype=_BF16, device=s_x.device)
+            if stream is not None:
+                _fb_keep(h, stream)
         else:
-            _fb_check("h", h, (_BF16,), (M, F), dev)
-    _fb_call(dev, stream, lib().dfk_swiglu_gate_up_fp8_block, _ptr(q_x), _ptr(s_x), _ptr(q_gate),
-             _ptr(s_gate), _ptr(q_up), _ptr(s_up), _ptr(h), _ptr(q_h), _ptr(s_h), M, D, F)
+            _fb_check("h", h, _BF16_ONLY, (M, F), dev)
+        ph, pq, ps = h.data_ptr(), None, None
+    _fb_call(dev, stream, lib().dfk_swiglu_gate_up_fp8_block, q_x.data_ptr(), s_x.data_ptr(),
+             q_gate.data_ptr(), s_gate.data_ptr(), q_up.data_ptr(), s_up.data_ptr(), ph, pq, ps,
+             M, D, F)
     return (q_h, s_h) if fp8_out else h
 
 

@@ -159,6 +159,7 @@ constexpr int FB_NORM_MAX_D = 32768  /* 4 chunks of 8 in each of 1024 threads */
 const void *fb_small_kernel(int nmat, int bn);
 int fb_small_threads(int nmat, int bn);
 int fb_small_smem(int nmat, int bn, int stages);
+int fb_small_min_stages(int nmat, int bn);
 
 // fp8_block_large.cu
 const void *fb_large_kernel_fn(bool gate);

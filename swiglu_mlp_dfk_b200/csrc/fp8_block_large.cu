@@ -27,9 +27,9 @@
 namespace dfk {
 
 constexpr int FBL_THREADS = 384;   // TMA, MMA and two scale warps; eight epilogue warps
-// Registers a thread: 384 x 168 at launch, then 40 for the first warpgroup and
-// 232 for the two epilogue warpgroups (40 + 2 x 232 = 3 x 168).
-constexpr int FBL_REGS_IO = 40, FBL_REGS_EPI = 232;
+// Registers a thread: 384 x 168 at launch, then 56 for the first warpgroup and
+// 224 for the two epilogue warpgroups (56 + 2 x 224 = 3 x 168).
+constexpr int FBL_REGS_IO = 56, FBL_REGS_EPI = 224;
 constexpr int FBL_STAGES = 6;
 constexpr int FBL_HALF = 128 * 128;           // bytes of one operand's half tile
 constexpr int FBL_STAGE = 2 * FBL_HALF;
@@ -43,7 +43,7 @@ constexpr int FBL_OFF_SW = FBL_OFF_SX + FBL_AHEAD * 512;   // [AHEAD][2 warps][2
 constexpr int FBL_OFF_COMB = FBL_OFF_SW + FBL_AHEAD * 16;  // [COMB][2][128] s_x s_w
 constexpr int FBL_OFF_MAX = FBL_OFF_COMB + FBL_COMB * 1024;  // [2 tiles][2][128] row maxima
 constexpr int FBL_OFF_BAR = FBL_OFF_MAX + 2048;
-constexpr int FBL_BARS = 2 * FBL_STAGES + 9;
+constexpr int FBL_BARS = 2 * FBL_STAGES + 13;
 constexpr int FBL_SMEM = 1024 + FBL_OFF_BAR + FBL_BARS * 8 + 16;
 
 // ---- cta_group::2 forms
@@ -103,32 +103,38 @@ __device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar) {
                : "memory");
 }
 
-// 32 TMEM columns of this warp's lanes; the values may be used after
-// tmem_wait32, which takes them as operands.
-__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
+// 16 TMEM columns of this warp's lanes; the values may be used after
+// tmem_wait16, which takes them as operands.
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
   asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
-      "%11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, "
-      "%28, %29, %30, %31}, [%32];"
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
+      "%11, %12, %13, %14, %15}, [%16];"
       : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
         "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]),
-        "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]),
-        "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
-        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]),
-        "=r"(r[31])
+        "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
       : "r"(taddr)
       : "memory");
 }
-__device__ __forceinline__ void tmem_wait32(uint32_t (&r)[32]) {
+__device__ __forceinline__ void tmem_wait16(uint32_t (&r)[16]) {
   asm volatile("tcgen05.wait::ld.sync.aligned;"
                : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]),
                  "+r"(r[6]), "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]),
-                 "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]), "+r"(r[16]), "+r"(r[17]),
-                 "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]),
-                 "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27])
+                 "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
                :
                : "memory");
-  asm volatile("" : "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31])::"memory");
+}
+
+// Whether the phase has completed, without waiting.
+__device__ __forceinline__ bool mbar_test(uint64_t *bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_addr(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
 }
 
 __device__ __forceinline__ void cp_async4(uint32_t dst, const float *src) {
@@ -204,9 +210,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(FBL_THREADS, 1)
 
   uint64_t *fullb = reinterpret_cast<uint64_t *>(smem + FBL_OFF_BAR);  // the leader's count
   uint64_t *empty = fullb + S;
-  uint64_t *accfull = empty + S;    // [2]
-  uint64_t *accempty = accfull + 2; // [2], the leader's count
-  uint64_t *maxfull = accempty + 2; // [4] row maxima of both halves written, per lane quarter
+  uint64_t *accfull = empty + S;    // [2 buffers][2 halves]
+  uint64_t *accempty = accfull + 4; // [2][2], the leader's count
+  uint64_t *maxfull = accempty + 4; // [4] row maxima of both halves written, per lane quarter
   uint64_t *done = maxfull + 4;
   volatile int *s_abort = reinterpret_cast<volatile int *>(done + 1);
   int *s_issued = reinterpret_cast<int *>(done + 1) + 1;
@@ -223,9 +229,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(FBL_THREADS, 1)
       mbar_init(&fullb[s], 1);
       mbar_init(&empty[s], 1);
     }
-    for (int s = 0; s < 2; ++s) {
-      mbar_init(&accfull[s], 3);    // the MMAs of a group and both scale warps
-      mbar_init(&accempty[s], 16);  // eight epilogue warps of each CTA
+    for (int s = 0; s < 4; ++s) {
+      mbar_init(&accfull[s], 3);   // the MMAs of a group's half and both scale warps
+      mbar_init(&accempty[s], 8);  // four epilogue warps of each CTA
     }
     for (int s = 0; s < 4; ++s) mbar_init(&maxfull[s], 2);
     mbar_init(done, 1);
@@ -281,31 +287,41 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(FBL_THREADS, 1)
     // ---- MMA, the leader CTA for both: 4 instructions of K = 32 per group
     const uint32_t leader = elect_one_sync();
     if (rank == 0) {
-      const uint32_t idesc = umma_idesc_e4m3_f32(256, 256);
+      const uint32_t idesc = umma_idesc_e4m3_f32(256, 128);
       const uint64_t desc0 = umma_desc_sw128(sbase);
-      int it = 0;
+      int it = 0, st = 0;
+      uint32_t ph = 0;
       bool ok = true;
       for (int t = pair; ok && t < ntiles; t += npairs) {
         for (int kb = 0; kb < p.G; ++kb, ++it) {
-          const int st = it % S, ab = it & 1;
-          ok = fb_wait(&fullb[st], (it / S) & 1, s_abort, p.err);
-          if (ok && it >= 2)
-            ok = fb_wait(&accempty[ab], ((it >> 1) - 1) & 1, s_abort, p.err);
-          ok = __all_sync(0xffffffffu, ok);
-          if (!ok) break;
+          const int ab = it & 1;
+          ok = fb_wait(&fullb[st], ph, s_abort, p.err);
+          if (!__all_sync(0xffffffffu, ok)) break;
           tc_fence_after();
           const uint64_t da = desc0 + (static_cast<uint32_t>(st * FBL_STAGE) >> 4);
-          const uint64_t db = da + (FBL_HALF >> 4);
 #pragma unroll
-          for (int kk = 0; kk < 4; ++kk)
-            if (leader)
-              umma_e4m3_pair(tmem + static_cast<uint32_t>(ab * 256), da + 2 * kk, db + 2 * kk,
-                             idesc, kk > 0 ? 1u : 0u);
-          if (leader) {
-            umma_commit_pair(&empty[st]);
-            umma_commit_pair(&accfull[ab]);
+          for (int h = 0; h < 2; ++h) {
+            ok = it < 2 || fb_wait(&accempty[2 * ab + h], ((it >> 1) - 1) & 1, s_abort, p.err);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
+            tc_fence_after();
+            // rows 64 h .. 64 h + 63 of each CTA's 128 weight rows
+            const uint64_t db = da + ((FBL_HALF + h * 64 * 128) >> 4);
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk)
+              if (leader)
+                umma_e4m3_pair(tmem + static_cast<uint32_t>(ab * 256 + h * 128), da + 2 * kk,
+                               db + 2 * kk, idesc, kk > 0 ? 1u : 0u);
+            if (leader) umma_commit_pair(&accfull[2 * ab + h]);
+            __syncwarp();
           }
+          if (!ok) break;
+          if (leader) umma_commit_pair(&empty[st]);
           __syncwarp();
+          if (++st == S) {
+            st = 0;
+            ph ^= 1u;
+          }
         }
       }
       if (leader) umma_commit_pair(done);
@@ -361,11 +377,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(FBL_THREADS, 1)
       const float x0 = s_sx[slot * 128 + row], x1 = s_sx[slot * 128 + row + 32];
       const float w0 = s_sw[slot * 4], w1 = s_sw[slot * 4 + 1];
       fetch();  // into the slot of the group before this one
-      // One barrier tells the epilogue that a group's sums and its scales are
+      // One barrier tells the epilogue that a half's sums and its scales are
       // there.  Group it - 2 is complete before `it` arrives on the same
-      // barrier; its MMAs followed the epilogue's release of group it - 4, the
+      // barriers; its MMAs followed the epilogue's release of group it - 4, the
       // last to use this slot.
-      const bool ok = it < 2 || fb_wait(&accfull[it & 1], ((it >> 1) - 1) & 1, s_abort, p.err);
+      uint64_t *full = &accfull[2 * (it & 1)];
+      const uint32_t before = ((it >> 1) - 1) & 1;
+      const bool ok = it < 2 || (fb_wait(&full[0], before, s_abort, p.err) &&
+                                 fb_wait(&full[1], before, s_abort, p.err));
       if (!__all_sync(0xffffffffu, ok)) break;
       float *c = s_comb + cs * 256 + row;
       c[0] = x0 * w0;
@@ -373,66 +392,65 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(FBL_THREADS, 1)
       c[128] = x0 * w1;
       c[160] = x1 * w1;
       __syncwarp();
-      if (lane == 0) mbar_arrive(&accfull[it & 1]);
+      if (lane < 2) mbar_arrive(&full[lane]);
     }
     cp_async_wait<0>();
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(FBL_REGS_EPI));
-    // ---- epilogue: thread = one token (TMEM lane) and half of the columns
+    // ---- epilogue: thread = one token (TMEM lane) and half of the columns, 64 of
+    // each CTA's weight rows (gated: 64 gate and the 64 matching up columns)
     const int ew = warp - 4, half = ew >> 2, q = warp & 3;
     const int row = 32 * q + lane;
     const uint32_t base = tmem + (static_cast<uint32_t>(32 * q) << 16);
     const float *s_comb = reinterpret_cast<const float *>(smem + FBL_OFF_COMB) + row;
     float *s_max = reinterpret_cast<float *>(smem + FBL_OFF_MAX);
     uint8_t *obuf = smem + FBL_OFF_OUT + ew * 2048;
-    const uint32_t empty_at[2] = {cluster_map(smem_addr(&accempty[0]), 0),
-                                  cluster_map(smem_addr(&accempty[1]), 0)};
+    const uint32_t empty_at = cluster_map(smem_addr(&accempty[half]), 0);
     pdl_wait();  // the outputs may still be read by the previous kernel
 
     int it = 0, nth = 0;
-    bool ok = true;
+    bool ok = true, rdy = false;
     for (int t = pair; ok && t < ntiles; t += npairs, ++nth) {
       uint64_t acc[64];  // pairs of neighbouring columns
 #pragma unroll
       for (int i = 0; i < 64; ++i) acc[i] = 0ull;
-      // A step waits for 32 columns, sends for the next 32 (past the end of a
-      // group: the next group's first, once it is complete) and adds the ones
-      // that are there, so a load is always on its way.
-      uint32_t d[2][32];
-      auto ready = [&]() {
-        ok = __all_sync(0xffffffffu, fb_wait(&accfull[it & 1], (it >> 1) & 1, s_abort, p.err));
-        tc_fence_after();
-        return ok;
-      };
-      const uint32_t tb = base + (GATE ? 64 : 128) * half;
-      if (!ready()) break;
-      tmem_ld32(tb + (it & 1) * 256, d[0]);
+      // One group at a time, 16 columns a step, the next 16 on their way; the
+      // next group's barrier is tested in the shadow of the last sums.
+      const uint32_t tb = base + 128 * half;
 #pragma unroll 1
-      for (int kb = 0;;) {
-        const int ab = it & 1, cs = it & (FBL_COMB - 1);
-        const float s0 = s_comb[cs * 256 + (GATE ? 0 : 128 * half)];
-        const float s1 = GATE ? s_comb[cs * 256 + 128] : s0;
+      for (int kb = 0; kb < p.G; ++kb) {
+        const int ab = it & 1;
+        if (!rdy) {
+          ok = fb_wait(&accfull[2 * ab + half], (it >> 1) & 1, s_abort, p.err);
+          if (!__all_sync(0xffffffffu, ok)) {
+            ok = false;
+            break;
+          }
+        }
+        tc_fence_after();
+        uint32_t d[2][16];
+        tmem_ld16(tb + ab * 256, d[0]);
+        const float *sc = s_comb + (it & (FBL_COMB - 1)) * 256;
+        const float s0 = sc[0], s1 = sc[128];
+        ++it;
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          tmem_wait32(d[c & 1]);
-          if (c < 3) {
-            tmem_ld32(tb + ab * 256 + (GATE && c >= 1 ? 32 * (c + 1) + 64 : 32 * (c + 1)),
-                      d[(c + 1) & 1]);
+        for (int c = 0; c < 8; ++c) {
+          tmem_wait16(d[c & 1]);
+          if (c < 7) {
+            tmem_ld16(tb + ab * 256 + 16 * (c + 1), d[(c + 1) & 1]);
           } else {
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive_cluster(empty_at[ab]);
-            ++it;
-            if (++kb < p.G && ready()) tmem_ld32(tb + (it & 1) * 256, d[0]);
+            if (lane == 0) mbar_arrive_cluster(empty_at + 16 * ab);
+            rdy = __all_sync(0xffffffffu, mbar_test(&accfull[2 * (it & 1) + half], (it >> 1) & 1));
           }
-          const uint64_t sc = c < 2 ? pack_f32x2(s0, s0) : pack_f32x2(s1, s1);
+          const uint64_t cc = c < 4 ? pack_f32x2(s0, s0) : pack_f32x2(s1, s1);
 #pragma unroll
-          for (int e = 0; e < 16; ++e)
-            acc[16 * c + e] = fma_f32x2(
+          for (int e = 0; e < 8; ++e)
+            acc[8 * c + e] = fma_f32x2(
                 pack_f32x2(__uint_as_float(d[c & 1][2 * e]), __uint_as_float(d[c & 1][2 * e + 1])),
-                sc, acc[16 * c + e]);
+                cc, acc[8 * c + e]);
         }
-        if (kb == p.G || !ok) break;
       }
       if (!ok) break;
       // ---- the tile's output
@@ -440,7 +458,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(FBL_THREADS, 1)
       tiles.at(t, tm, tn);
       const int m0 = tm * 256 + static_cast<int>(rank) * 128 + 32 * q;  // the warp's first row
       if constexpr (!GATE) {
-        const int n0 = tn * 256 + 128 * half;
+        const int n0 = tn * 256 + 64 * half;
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
           uint32_t w[16];
@@ -451,7 +469,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(FBL_THREADS, 1)
             w[e] = pack_bf16x2(lo, hi);
           }
           fbl_rows64(obuf, lane, w, [&](int r, int cc, const uint4 &v) {
-            fbl_store_bf16(p, m0 + r, n0 + 32 * c + 8 * cc, v);
+            fbl_store_bf16(p, m0 + r, n0 + (c & 1) * 32 + (c >> 1) * 128 + 8 * cc, v);
           });
         }
       } else {

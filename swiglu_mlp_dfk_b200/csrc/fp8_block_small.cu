@@ -18,21 +18,54 @@
 
 namespace dfk {
 
-constexpr int FBS_THREADS = 192;   // TMA warp, MMA warp, four epilogue warps
 constexpr int FBS_WTILE = 128 * 128;
 constexpr int FBS_PRE = 4;         // groups whose scales are loaded ahead
 
 template <int NMAT, int BN>
 struct FbsShape {
+  // epilogue warps: one for each TMEM lane quarter, two where four would have
+  // more than 64 sums a thread (64 tokens of a gated product: 27 us with four
+  // warps, 32 columns of each matrix every 60 cycles, against 21 with eight)
+  static constexpr int warps = NMAT * BN > 64 ? 8 : 4;
+  static constexpr int threads = 64 + 32 * warps;  // TMA warp, MMA warp
+  static constexpr int tokens = BN * 4 / warps;    // of one epilogue thread
   static constexpr int stage_bytes = NMAT * FBS_WTILE + BN * 128;
   static constexpr int acc_cols = NMAT * BN;       // one TMEM buffer
   static constexpr int tmem_cols = 2 * acc_cols < 32 ? 32 : 2 * acc_cols;
-  static constexpr int comb_floats = 4 * 2 * NMAT * BN;  // per warp, two groups
+  static constexpr int comb_floats = warps * 2 * NMAT * tokens;  // per warp, two groups
   static constexpr int part_bytes = NMAT * BN * 128 * 4;
+  static constexpr int min_stages =
+      part_bytes > 2 * stage_bytes ? (part_bytes + stage_bytes - 1) / stage_bytes : 2;
 };
 
+// 16 or 32 TMEM columns of this warp's lanes; the values may be used after
+// tmem_ld_wait.
+template <int N>
+__device__ __forceinline__ void tmem_cols(uint32_t taddr, float (&d)[N]) {
+  static_assert(N == 16 || N == 32, "columns a load");
+  if constexpr (N == 16) {
+    tmem_ld_32x32b_x16(taddr, d);
+  } else {
+    uint32_t r[32];
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
+        "%11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, "
+        "%28, %29, %30, %31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+          "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]),
+          "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]),
+          "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+          "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]),
+          "=r"(r[31])
+        : "r"(taddr)
+        : "memory");
+#pragma unroll
+    for (int i = 0; i < 32; ++i) d[i] = __uint_as_float(r[i]);
+  }
+}
+
 template <int NMAT, int BN>
-__global__ void __launch_bounds__(FBS_THREADS)
+__global__ void __launch_bounds__(FbsShape<NMAT, BN>::threads)
     fb_small_kernel_t(const __grid_constant__ FbMaps maps, const FbParams p) {
   using Sh = FbsShape<NMAT, BN>;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
@@ -69,7 +102,7 @@ __global__ void __launch_bounds__(FBS_THREADS)
     }
     for (int s = 0; s < 2; ++s) {
       mbar_init(&accfull[s], 1);
-      mbar_init(&accempty[s], 4);
+      mbar_init(&accempty[s], Sh::warps);
     }
     mbar_init(done, 1);
     *s_abort = 0;
@@ -93,26 +126,32 @@ __global__ void __launch_bounds__(FBS_THREADS)
       const uint64_t pol_w = gridDim.y > 1 ? l2_policy_evict_normal() : l2_policy_evict_first();
       const uint64_t pol_x = l2_policy_evict_normal();
       const int S0 = min(S, nkb);
-      auto load_w = [&](int i) {
-        uint8_t *sb = smem + static_cast<size_t>(i % S) * Sh::stage_bytes;
-        mbar_arrive_expect_tx(&fullb[i % S], Sh::stage_bytes);
+      auto load_w = [&](int i, int st) {
+        uint8_t *sb = smem + st * Sh::stage_bytes;
+        mbar_arrive_expect_tx(&fullb[st], Sh::stage_bytes);
 #pragma unroll
         for (int m = 0; m < NMAT; ++m)
-          tma_load_2d(sb + m * FBS_WTILE, &maps.w[m], &fullb[i % S], (kb0 + i) * 128, j0, pol_w);
+          tma_load_2d(sb + m * FBS_WTILE, &maps.w[m], &fullb[st], (kb0 + i) * 128, j0, pol_w);
       };
-      auto load_x = [&](int i) {
-        uint8_t *sb = smem + static_cast<size_t>(i % S) * Sh::stage_bytes;
-        tma_load_2d(sb + NMAT * FBS_WTILE, &maps.x, &fullb[i % S], (kb0 + i) * 128, n0, pol_x);
+      auto load_x = [&](int i, int st) {
+        tma_load_2d(smem + st * Sh::stage_bytes + NMAT * FBS_WTILE, &maps.x, &fullb[st],
+                    (kb0 + i) * 128, n0, pol_x);
       };
-      for (int i = 0; i < S0; ++i) load_w(i);
+      for (int i = 0; i < S0; ++i) load_w(i, i);
       pdl_wait();
-      for (int i = 0; i < S0; ++i) load_x(i);
-      int issued = S0;
+      for (int i = 0; i < S0; ++i) load_x(i, i);
+      int issued = S0, st = 0;
+      uint32_t ph = 0;  // of the stage's last use; stages and phases are counted along:
+                        // S is no constant, and a division costs as much as a wait
       for (int i = S0; i < nkb; ++i) {
-        if (!fb_wait(&empty[i % S], ((i / S) - 1) & 1, s_abort, p.err)) break;
-        load_w(i);
-        load_x(i);
+        if (!fb_wait(&empty[st], ph, s_abort, p.err)) break;
+        load_w(i, st);
+        load_x(i, st);
         issued = i + 1;
+        if (++st == S) {
+          st = 0;
+          ph ^= 1u;
+        }
       }
       *s_issued = issued;
     }
@@ -122,10 +161,12 @@ __global__ void __launch_bounds__(FBS_THREADS)
     const uint32_t leader = elect_one_sync();
     const uint32_t idesc = umma_idesc_e4m3_f32(128, BN);
     const uint64_t desc0 = umma_desc_sw128(sbase);
+    int st = 0;
+    uint32_t ph = 0;
     for (int i = 0; i < nkb; ++i) {
-      const int st = i % S, ab = i & 1;
-      bool ok = fb_wait(&fullb[st], (i / S) & 1, s_abort, p.err);
-      if (ok && i >= 2) ok = fb_wait(&accempty[ab], ((i >> 1) - 1) & 1, s_abort, p.err);
+      const int ab = i & 1;
+      bool ok = i < 2 || fb_wait(&accempty[ab], ((i >> 1) - 1) & 1, s_abort, p.err);
+      ok = ok && fb_wait(&fullb[st], ph, s_abort, p.err);
       if (!__all_sync(0xffffffffu, ok)) break;
       tc_fence_after();
       const uint64_t ds = desc0 + (static_cast<uint32_t>(st * Sh::stage_bytes) >> 4);
@@ -142,21 +183,27 @@ __global__ void __launch_bounds__(FBS_THREADS)
         umma_commit(&accfull[ab]);
       }
       __syncwarp();
+      if (++st == S) {
+        st = 0;
+        ph ^= 1u;
+      }
     }
     if (leader) umma_commit(done);
     __syncwarp();
   } else {
-    // ---- epilogue warps 2..5: TMEM lane quarter = warp mod 4
+    // ---- epilogue warps: TMEM lane quarter = warp mod 4, a share of the tokens
     const int ew = warp - 2, q = warp & 3;
     const int row = 32 * q + lane;
-    const uint32_t base = tmem + (static_cast<uint32_t>(32 * q) << 16);
-    constexpr int SL = (BN + 31) / 32;  // tokens a lane loads scales for
-    float *comb = s_comb + ew * 2 * NMAT * BN;
-    float acc[NMAT][BN];
+    constexpr int TN = Sh::tokens;
+    const int t0 = (ew >> 2) * TN;  // the warp's first token
+    const uint32_t base = tmem + (static_cast<uint32_t>(32 * q) << 16) + t0;
+    constexpr int SL = (TN + 31) / 32;  // tokens a lane loads scales for
+    float *comb = s_comb + ew * 2 * NMAT * TN;
+    float acc[NMAT][TN];
 #pragma unroll
     for (int m = 0; m < NMAT; ++m)
 #pragma unroll
-      for (int n = 0; n < BN; ++n) acc[m][n] = 0.f;
+      for (int n = 0; n < TN; ++n) acc[m][n] = 0.f;
     float psx[FBS_PRE][SL], psw[FBS_PRE][NMAT];
     pdl_wait();  // s_x comes from the previous kernel
     auto fetch = [&](int i, float (&sx)[SL], float (&sw)[NMAT]) {
@@ -166,9 +213,9 @@ __global__ void __launch_bounds__(FBS_THREADS)
         sw[m] = i < nkb ? __ldg(p.sw[m] + static_cast<size_t>(blk) * p.G + kb) : 0.f;
 #pragma unroll
       for (int e = 0; e < SL; ++e) {
-        const int n = n0 + lane + 32 * e;
+        const int n = n0 + t0 + lane + 32 * e;
         sx[e] = 0.f;
-        if (i < nkb && lane + 32 * e < BN && n < p.M && DFK_IN_BOUNDS(kb < p.G, 27, p.err))
+        if (i < nkb && lane + 32 * e < TN && n < p.M && DFK_IN_BOUNDS(kb < p.G, 27, p.err))
           sx[e] = __ldg(p.sx + static_cast<size_t>(kb) * p.M + n);
       }
     };
@@ -182,34 +229,37 @@ __global__ void __launch_bounds__(FBS_THREADS)
         if (go && i < nkb) {
           const int ab = u & 1;  // FBS_PRE is even: the same as i & 1
           // this group's s_x s_w, one per token, for the whole warp
-          float *cb = comb + ab * NMAT * BN;
+          float *cb = comb + ab * NMAT * TN;
 #pragma unroll
           for (int m = 0; m < NMAT; ++m)
 #pragma unroll
             for (int e = 0; e < SL; ++e)
-              if (BN >= 32 || lane < BN) cb[m * BN + lane + 32 * e] = psx[u][e] * psw[u][m];
+              if (TN >= 32 || lane < TN) cb[m * TN + lane + 32 * e] = psx[u][e] * psw[u][m];
           fetch(i + FBS_PRE, psx[u], psw[u]);
           __syncwarp();
           go = __all_sync(0xffffffffu, fb_wait(&accfull[ab], (i >> 1) & 1, s_abort,
                                                          p.err));
           if (go) {
             tc_fence_after();
+            constexpr int CH = TN < 32 ? TN : 32;
 #pragma unroll
-            for (int m = 0; m < NMAT; ++m)
+            for (int c = 0; c < TN; c += CH) {
+              float d[NMAT][CH];
 #pragma unroll
-              for (int c = 0; c < BN; c += 16) {
-                float d[16];
-                tmem_ld_32x32b_x16(base + ab * Sh::acc_cols + m * BN + c, d);
-                tmem_ld_wait();
+              for (int m = 0; m < NMAT; ++m)
+                tmem_cols<CH>(base + ab * Sh::acc_cols + m * BN + c, d[m]);
+              tmem_ld_wait();
 #pragma unroll
-                for (int e = 0; e < 16; e += 4) {
-                  const float4 w = *reinterpret_cast<const float4 *>(cb + m * BN + c + e);
-                  acc[m][c + e + 0] = fmaf(d[e + 0], w.x, acc[m][c + e + 0]);
-                  acc[m][c + e + 1] = fmaf(d[e + 1], w.y, acc[m][c + e + 1]);
-                  acc[m][c + e + 2] = fmaf(d[e + 2], w.z, acc[m][c + e + 2]);
-                  acc[m][c + e + 3] = fmaf(d[e + 3], w.w, acc[m][c + e + 3]);
+              for (int m = 0; m < NMAT; ++m)
+#pragma unroll
+                for (int e = 0; e < CH; e += 4) {
+                  const float4 w = *reinterpret_cast<const float4 *>(cb + m * TN + c + e);
+                  acc[m][c + e + 0] = fmaf(d[m][e + 0], w.x, acc[m][c + e + 0]);
+                  acc[m][c + e + 1] = fmaf(d[m][e + 1], w.y, acc[m][c + e + 1]);
+                  acc[m][c + e + 2] = fmaf(d[m][e + 2], w.z, acc[m][c + e + 2]);
+                  acc[m][c + e + 3] = fmaf(d[m][e + 3], w.w, acc[m][c + e + 3]);
                 }
-              }
+            }
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&accempty[ab]);
@@ -224,7 +274,7 @@ __global__ void __launch_bounds__(FBS_THREADS)
 #pragma unroll
       for (int m = 0; m < NMAT; ++m)
 #pragma unroll
-        for (int n = 0; n < BN; ++n) part[(m * BN + n) * 128 + row] = acc[m][n];
+        for (int n = 0; n < TN; ++n) part[(m * BN + t0 + n) * 128 + row] = acc[m][n];
   }
 
   // TMEM is released and the copies in flight are waited for before the
@@ -251,7 +301,7 @@ __global__ void __launch_bounds__(FBS_THREADS)
     // one token per warp and turn, spread over the cluster's CTAs; lane l
     // takes rows 4 l .. 4 l + 3
     const int nt = min(BN, p.M - n0);
-    for (int n = rank * 4 + (warp - 2); n < nt; n += 4 * ks) {
+    for (int n = rank * Sh::warps + (warp - 2); n < nt; n += Sh::warps * ks) {
       float a[NMAT][4];
 #pragma unroll
       for (int m = 0; m < NMAT; ++m) {
@@ -310,13 +360,15 @@ static int smem_of(int stages) {
   return 1024 + ring + Sh::comb_floats * 4 + (2 * stages + 5) * 8 + 16;
 }
 
-#define DFK_FBS_PICK(expr)                                   \
-  (nmat == 1 ? (bn == 16   ? expr(1, 16)                     \
-                : bn == 32 ? expr(1, 32)                     \
-                           : expr(1, 64))                    \
-             : (bn == 16   ? expr(2, 16)                     \
-                : bn == 32 ? expr(2, 32)                     \
-                           : expr(2, 64)))
+#define DFK_FBS_PICK(expr)               \
+  (nmat == 1 ? (bn == 16    ? expr(1, 16)  \
+                : bn == 32  ? expr(1, 32)  \
+                : bn == 64  ? expr(1, 64)  \
+                            : expr(1, 128)) \
+             : (bn == 16    ? expr(2, 16)  \
+                : bn == 32  ? expr(2, 32)  \
+                : bn == 64  ? expr(2, 64)  \
+                            : expr(2, 128)))
 
 const void *fb_small_kernel(int nmat, int bn) {
 #define DFK_FBS_FN(NM, B) reinterpret_cast<const void *>(&fb_small_kernel_t<NM, B>)
@@ -324,7 +376,17 @@ const void *fb_small_kernel(int nmat, int bn) {
 #undef DFK_FBS_FN
 }
 
-int fb_small_threads(int, int) { return FBS_THREADS; }
+int fb_small_threads(int nmat, int bn) {
+#define DFK_FBS_TH(NM, B) FbsShape<NM, B>::threads
+  return DFK_FBS_PICK(DFK_FBS_TH);
+#undef DFK_FBS_TH
+}
+
+int fb_small_min_stages(int nmat, int bn) {
+#define DFK_FBS_MS(NM, B) FbsShape<NM, B>::min_stages
+  return DFK_FBS_PICK(DFK_FBS_MS);
+#undef DFK_FBS_MS
+}
 
 int fb_small_smem(int nmat, int bn, int stages) {
 #define DFK_FBS_SM(NM, B) smem_of<NM, B>(stages)
