@@ -35,22 +35,34 @@ struct FbScale {
   float sr;   // s in the residual; 0 for an infinite s, where inv is 0 too
 };
 
-__device__ __forceinline__ FbScale fb_scale(float amax) {
-  FbScale f;
-  f.s = max_nan(amax / FB_E4M3_MAX, 1.17549435e-38f);
-  f.inv = 1.0f / f.s;
-  f.sr = f.s > 3.402823466e38f ? 0.f : f.s;
-  return f;
+// v / b rounded to nearest, from b's correctly rounded reciprocal y and one
+// residual step (Markstein, "Computation of elementary functions on the IBM
+// RISC System/6000 processor", 1990): u = v y, u + (v - u b) y.  bf16 inputs
+// often make v / s a tie between two codes, so the plain product v y, off by
+// an ulp, would round a few codes in a thousand the other way.
+__device__ __forceinline__ float fb_divide(float v, float b, float y) {
+  const float u = v * y;
+  return fmaf(fmaf(-u, b, v), y, u);
 }
 
-// v / s rounded to nearest, from the correctly rounded reciprocal and one
-// residual step (Markstein, "Computation of elementary functions on the IBM
-// RISC System/6000 processor", 1990): u = v y, u + (v - u s) y with y = 1/s.
-// bf16 inputs often make v / s a tie between two codes, so the plain product
-// v y, off by an ulp, would round a few codes in a thousand the other way.
+// The scale of a group: max(amax / 448, 2^-126), amax / 448 rounded to nearest;
+// infinite for an infinite amax, NaN for a NaN.
+__device__ __forceinline__ float fb_group_scale(float amax) {
+  const float s = fb_divide(amax, FB_E4M3_MAX, 1.0f / FB_E4M3_MAX);
+  return amax > 3.402823466e38f ? amax : max_nan(s, 1.17549435e-38f);
+}
+
+__device__ __forceinline__ FbScale fb_scale_of(float s, float inv) {
+  return FbScale{s, inv, s > 3.402823466e38f ? 0.f : s};
+}
+
+__device__ __forceinline__ FbScale fb_scale(float amax) {
+  const float s = fb_group_scale(amax);
+  return fb_scale_of(s, 1.0f / s);
+}
+
 __device__ __forceinline__ float fb_quotient(float v, const FbScale &f) {
-  const float u = v * f.inv;
-  return fmaf(fmaf(-u, f.sr, v), f.inv, u);
+  return fb_divide(v, f.sr, f.inv);
 }
 
 // Four values -> four E4M3 codes, element 0 in the low byte.

@@ -30,11 +30,27 @@ __device__ __forceinline__ void unpack8(const uint4 &w, float (&v)[8]) {
   }
 }
 
-constexpr int FBQ_THREADS = 256;
+__device__ __forceinline__ uint32_t max_nan_bf16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+
+// max |v| of eight bf16 values, in the low half.
+__device__ __forceinline__ uint32_t bf16x2_abs_max(const uint4 &w) {
+  const uint32_t m = 0x7fff7fffu;
+  const uint32_t a = max_nan_bf16x2(max_nan_bf16x2(w.x & m, w.y & m),
+                                    max_nan_bf16x2(w.z & m, w.w & m));
+  return max_nan_bf16x2(a, a >> 16);
+}
+
+constexpr int FBQ_THREADS = 128;
 constexpr int FBQ_ROWS = 4;
 
 // Half a warp takes one group of 128 of FBQ_ROWS consecutive rows: 16 bytes a
-// lane and row, every load issued before the first use.
+// lane and row, every load issued before the first use.  Bound by memory: 2047
+// rows of 14336 in 14.7 us, 92 % of the copy rate (17.2 us when every lane worked
+// out every row's scale and maximum in fp32: 13 instructions an element).
 __global__ void __launch_bounds__(FBQ_THREADS)
     fb_quant_kernel(const uint16_t *__restrict__ x, uint8_t *__restrict__ q,
                     float *__restrict__ s, int M, int K, int G, long long items, unsigned *err) {
@@ -55,18 +71,34 @@ __global__ void __launch_bounds__(FBQ_THREADS)
     if (in && m0 + r < M && DFK_IN_BOUNDS(k + 8 <= K, 20, err))
       w[r] = ld_nc_v4(x + static_cast<size_t>(m0 + r) * K + k);
   }
+  // Magnitudes stay in bf16 (exact) until the group's is known: two rows share
+  // a register in the butterfly over the 16 lanes.
+  uint32_t top[FBQ_ROWS / 2];
+#pragma unroll
+  for (int r = 0; r < FBQ_ROWS; r += 2)
+    top[r / 2] = __byte_perm(bf16x2_abs_max(w[r]), bf16x2_abs_max(w[r + 1]), 0x5410);
+#pragma unroll
+  for (int d = 8; d >= 1; d >>= 1)
+#pragma unroll
+    for (int r = 0; r < FBQ_ROWS / 2; ++r)
+      top[r] = max_nan_bf16x2(top[r], __shfl_xor_sync(0xffffffffu, top[r], d));
+  // Lane l works out the scale and the reciprocal of row l mod 4 and stores the
+  // scale (consecutive rows: one transaction); the others ask it.
+  static_assert(FBQ_ROWS == 4, "rows a lane selects from");
+  const uint32_t t01 = (l & 2) ? top[1] : top[0];
+  const float mine = fb_group_scale((l & 1) ? bf16_hi(t01) : bf16_lo(t01));
+  const float mine_inv = 1.0f / mine;
+  if (l < FBQ_ROWS && m0 + l < M && DFK_IN_BOUNDS(g < G, 22, err))
+    s[static_cast<size_t>(g) * M + m0 + l] = mine;
 #pragma unroll
   for (int r = 0; r < FBQ_ROWS; ++r) {
+    const FbScale f = fb_scale_of(__shfl_sync(0xffffffffu, mine, r, 16),
+                                  __shfl_sync(0xffffffffu, mine_inv, r, 16));
     float v[8];
     unpack8(w[r], v);
-    const FbScale f = fb_scale(group_max(abs_max8(v)));
-    if (m0 + r < M) {
-      if (in && DFK_IN_BOUNDS(k + 8 <= K, 21, err))
-        *reinterpret_cast<uint2 *>(q + static_cast<size_t>(m0 + r) * K + k) =
-            make_uint2(fb_codes4(v[0], v[1], v[2], v[3], f), fb_codes4(v[4], v[5], v[6], v[7], f));
-      if (l == 0 && DFK_IN_BOUNDS(g < G, 22, err))
-        s[static_cast<size_t>(g) * M + m0 + r] = f.s;
-    }
+    if (in && m0 + r < M && DFK_IN_BOUNDS(k + 8 <= K, 21, err))
+      *reinterpret_cast<uint2 *>(q + static_cast<size_t>(m0 + r) * K + k) =
+          make_uint2(fb_codes4(v[0], v[1], v[2], v[3], f), fb_codes4(v[4], v[5], v[6], v[7], f));
   }
 }
 
@@ -75,7 +107,14 @@ __global__ void __launch_bounds__(FBQ_THREADS)
 //   r = bf16(x + residual)      (stored; the norm reads the rounded sum, as
 //                                the next layer does)
 //   v = (r / sqrt(mean r^2 + eps)) * gamma, fp32, quantised per group.
-template <int CPT>
+//
+// LATE false (up to 1024 rows: latency counts): gamma is loaded before the
+// previous kernel has finished.  LATE true (more: bandwidth counts): gamma, which
+// L1 holds, is read when it is needed, so that its registers are free for
+// more threads.  4096 rows of 8192: 38.5 us, 93 % of the copy rate (two chunks a
+// thread and gamma early: 45 us); 2048 rows of 4096: 11.2 us against 12.4; one row
+// of 4096: 1.7 us early, 2.0 late; 1024 rows: the same.
+template <int CPT, bool LATE>
 __global__ void __launch_bounds__(1024)
     fb_norm_kernel(const uint16_t *x, const uint16_t *res, const uint16_t *__restrict__ gamma,
                    float eps, uint16_t *res_out, uint8_t *__restrict__ q,
@@ -85,7 +124,7 @@ __global__ void __launch_bounds__(1024)
   const int m = blockIdx.x;
   uint4 g[CPT];
 #pragma unroll
-  for (int i = 0; i < CPT; ++i) {
+  for (int i = 0; !LATE && i < CPT; ++i) {
     const int k = 8 * (tid + T * i);
     g[i] = make_uint4(0u, 0u, 0u, 0u);
     if (k < D) g[i] = ld_nc_v4(gamma + k);
@@ -110,11 +149,7 @@ __global__ void __launch_bounds__(1024)
     uint32_t *aw = &a[i].x, *bw = &b[i].x;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      if (res) {
-        const uint32_t lo = f32_to_bf16_bits(bf16_lo(aw[j]) + bf16_lo(bw[j]));
-        const uint32_t hi = f32_to_bf16_bits(bf16_hi(aw[j]) + bf16_hi(bw[j]));
-        aw[j] = lo | (hi << 16);
-      }
+      if (res) asm("add.rn.bf16x2 %0, %0, %1;" : "+r"(aw[j]) : "r"(bw[j]));
       const float f0 = bf16_lo(aw[j]), f1 = bf16_hi(aw[j]);
       ss = fmaf(f0, f0, ss);
       ss = fmaf(f1, f1, ss);
@@ -131,22 +166,56 @@ __global__ void __launch_bounds__(1024)
 #pragma unroll
   for (int d = 16; d >= 1; d >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, d);
   const float r = 1.0f / sqrtf(ss / static_cast<float>(D) + eps);
+  const uint32_t rb = __float_as_uint(r);
+  const float c = r == r ? __uint_as_float(rb & 0x7f800000u) : r;
+  const float t = __uint_as_float((rb & 0x007fffffu) | 0x3f800000u);
+  // r = c t, c a power of two and t in [1, 2): u = (a c) gamma is exact (a
+  // product of two bf16 factors), and t falls out of v / s, so that the codes
+  // depend on no rounding but that of 448 / max |u| -- unless the scale is at
+  // its floor.
+  float u[CPT][8], top[CPT];
 #pragma unroll
   for (int i = 0; i < CPT; ++i) {
     const int k = 8 * (tid + T * i);
-    float v[8], w[8];
-    unpack8(a[i], v);
+    float w[8];
+    unpack8(a[i], u[i]);
+    if (LATE) {
+      g[i] = make_uint4(0u, 0u, 0u, 0u);
+      if (k < D) g[i] = __ldg(reinterpret_cast<const uint4 *>(gamma + k));
+    }
     unpack8(g[i], w);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = k < D ? (v[j] * r) * w[j] : 0.f;
-    const FbScale f = fb_scale(group_max(abs_max8(v)));
-    if (k < D) {
-      if (DFK_IN_BOUNDS(k + 8 <= D && m < M, 25, err))
-        *reinterpret_cast<uint2 *>(q + row + k) =
-            make_uint2(fb_codes4(v[0], v[1], v[2], v[3], f), fb_codes4(v[4], v[5], v[6], v[7], f));
-      if ((tid & 15) == 0 && DFK_IN_BOUNDS(k / FB_GROUP < G, 26, err))
-        s[static_cast<size_t>(k / FB_GROUP) * M + m] = f.s;
+    for (int j = 0; j < 8; ++j) u[i][j] = (u[i][j] * c) * w[j];
+    if (k >= D) {  // c may be infinite or NaN: nothing of it in the padding
+#pragma unroll
+      for (int j = 0; j < 8; ++j) u[i][j] = 0.f;
     }
+    top[i] = group_max(abs_max8(u[i]));
+  }
+  // lane l mod CPT of the group's 16 works out the scale of chunk i = l mod CPT
+  const int l = tid & 15, li = l % CPT;
+  float mine = top[0];
+#pragma unroll
+  for (int i = 1; i < CPT; ++i) mine = li == i ? top[i] : mine;
+  const float s_v = fb_group_scale(mine * t);
+  float s_u = fb_group_scale(mine);
+  if (s_v == 1.17549435e-38f) s_u = s_v / t;
+  if (s_v != s_v) s_u = s_v;
+  const float inv = 1.0f / s_u;
+  {
+    const int k = 8 * (tid - l + T * li);  // the group's first element
+    if (l < CPT && k < D && DFK_IN_BOUNDS(k / FB_GROUP < G && m < M, 26, err))
+      s[static_cast<size_t>(k / FB_GROUP) * M + m] = s_v;
+  }
+#pragma unroll
+  for (int i = 0; i < CPT; ++i) {
+    const int k = 8 * (tid + T * i);
+    const FbScale f = fb_scale_of(__shfl_sync(0xffffffffu, s_u, i, 16),
+                                  __shfl_sync(0xffffffffu, inv, i, 16));
+    if (k < D && DFK_IN_BOUNDS(k + 8 <= D && m < M, 25, err))
+      *reinterpret_cast<uint2 *>(q + row + k) =
+          make_uint2(fb_codes4(u[i][0], u[i][1], u[i][2], u[i][3], f),
+                     fb_codes4(u[i][4], u[i][5], u[i][6], u[i][7], f));
   }
 }
 
@@ -171,11 +240,17 @@ cudaError_t launch_fb_norm(const void *x, const void *res, const void *gamma, fl
   uint8_t *qp = static_cast<uint8_t *>(q);
   int G = (D + FB_GROUP - 1) / FB_GROUP;
   const int chunks = D / 8;
-  const int cpt = chunks <= 512 ? 1 : chunks <= 2048 ? 2 : 4;
+  // many rows: four chunks a thread, 128 bytes on their way in each; few: as
+  // many threads as there are chunks, up to the two that 1024 threads leave
+  const bool late = M > 1024;
+  const int cpt = late ? 4 : chunks <= 512 ? 1 : chunks <= 2048 ? 2 : 4;
   const int T = ((chunks + cpt - 1) / cpt + 31) / 32 * 32;
-  const void *fn = cpt == 1   ? reinterpret_cast<const void *>(&fb_norm_kernel<1>)
-                   : cpt == 2 ? reinterpret_cast<const void *>(&fb_norm_kernel<2>)
-                              : reinterpret_cast<const void *>(&fb_norm_kernel<4>);
+#define DFK_FBN(C, L) reinterpret_cast<const void *>(&fb_norm_kernel<C, L>)
+  const void *fn = late       ? DFK_FBN(4, true)
+                   : cpt == 1 ? DFK_FBN(1, false)
+                   : cpt == 2 ? DFK_FBN(2, false)
+                              : DFK_FBN(4, false);
+#undef DFK_FBN
   void *args[] = {&xp, &rp, &gp, &eps, &op, &qp, &s, &M, &D, &G, &err};
   return launch_kernel(fn, dim3(M), dim3(T), 0, st, pdl, args);
 }
