@@ -142,6 +142,10 @@ __device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr) {
   return v;
 }
 
+__device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
+  return f32_to_bf16_bits(lo) | (static_cast<uint32_t>(f32_to_bf16_bits(hi)) << 16);
+}
+
 // ---- the products' arguments
 
 struct FbMaps {
@@ -160,6 +164,38 @@ struct FbParams {
   int stages;
 };
 
+// Output of one token's 128 weight rows (block `blk`) by a whole warp, four
+// rows a lane: bf16, or codes and the group's scale.
+template <int NMAT>
+__device__ __forceinline__ void fb_emit4(const FbParams &p, int m, int blk, int lane,
+                                         const float (&a)[NMAT][4]) {
+  const int j = blk * 128 + 4 * lane;
+  float h[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    h[e] = NMAT == 2 ? fb_silu_mul(a[0][e], a[NMAT - 1][e]) : a[0][e];
+    if (j + e >= p.N) h[e] = 0.f;
+  }
+  const size_t at = static_cast<size_t>(m) * p.N + j;
+  if (NMAT == 2 && p.y == nullptr) {
+    float mx = max_nan(max_nan(fabsf(h[0]), fabsf(h[1])), max_nan(fabsf(h[2]), fabsf(h[3])));
+#pragma unroll
+    for (int d = 16; d >= 1; d >>= 1) mx = max_nan(mx, __shfl_xor_sync(0xffffffffu, mx, d));
+    const FbScale f = fb_scale(mx);
+    if (j < p.N && DFK_IN_BOUNDS(j + 4 <= p.N && m < p.M, 28, p.err))
+      *reinterpret_cast<uint32_t *>(p.qh + at) = fb_codes4(h[0], h[1], h[2], h[3], f);
+    if (lane == 0) p.sh[static_cast<size_t>(blk) * p.M + m] = f.s;
+  } else if ((p.N & 3) == 0) {
+    if (j < p.N && DFK_IN_BOUNDS(j + 4 <= p.N && m < p.M, 29, p.err))
+      *reinterpret_cast<uint2 *>(p.y + at) = make_uint2(pack_bf16x2(h[0], h[1]),
+                                                        pack_bf16x2(h[2], h[3]));
+  } else {
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (j + e < p.N && DFK_IN_BOUNDS(m < p.M, 30, p.err)) p.y[at + e] = f32_to_bf16_bits(h[e]);
+  }
+}
+
 // kernels of fp8_block_quant.cu / fp8_block_small.cu
 cudaError_t launch_fb_quant(const void *x, void *q, float *s, int M, int K, unsigned *err,
                             cudaStream_t st, bool pdl);
@@ -173,9 +209,11 @@ int fb_small_threads(int nmat, int bn);
 int fb_small_smem(int nmat, int bn, int stages);
 int fb_small_min_stages(int nmat, int bn);
 
-// fp8_block_large.cu
-const void *fb_large_kernel_fn(bool gate);
-cudaError_t launch_fb_large(bool gate, const FbMaps &maps, const FbParams &p, int sms,
-                            cudaStream_t st, bool pdl);
+// fp8_block_large.cu: tiles of 256 tokens by pairs of CTAs (`pair`), or of 128 tokens
+// by CTAs of their own, `ks` of them to a tile
+const void *fb_large_kernel_fn(bool gate, bool pair);
+int fb_large_weight_box(bool pair);  // rows of the weights' TMA box
+cudaError_t launch_fb_large(bool gate, bool pair, int ks, const FbMaps &maps, const FbParams &p,
+                            int sms, cudaStream_t st, bool pdl);
 
 }  // namespace dfk

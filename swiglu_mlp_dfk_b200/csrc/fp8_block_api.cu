@@ -40,7 +40,7 @@ struct FbCall {
 
 static int launch_small(const FbCall &c, int sms, unsigned *err, cudaStream_t st) {
   const int G = (c.K + FB_GROUP - 1) / FB_GROUP;
-  const int bn = c.M <= 16 ? 16 : c.M <= 32 ? 32 : c.M <= 64 ? 64 : 128;
+  const int bn = c.M <= 16 ? 16 : c.M <= 32 ? 32 : 64;
   const int blocks = (c.N + 127) / 128, tiles = (c.M + bn - 1) / bn;
   if (tiles > 65535) return api_fail(DFK_ERR_UNSUPPORTED_SHAPE, "M=%d is too large", c.M);
   // Clusters of 1, 2, 4 or 8 CTAs a row block, each with four groups or more.
@@ -50,7 +50,7 @@ static int launch_small(const FbCall &c, int sms, unsigned *err, cudaStream_t st
   // Two matrices: one CTA on an SM with all of its shared memory (stages of
   // 32 KB and more), two where the row blocks outnumber the SMs.
   const long long work = static_cast<long long>(blocks) * tiles;
-  const bool pack = c.nmat == 1 ? bn < 128 : bn < 64 && work > sms;
+  const bool pack = c.nmat == 1 || (bn < 64 && work > sms);
   const int limit = pack ? 2 * sms : sms;
   int ks = 1;
   while (ks < 8 && work * ks * 2 <= limit && ks * 8 <= G) ks *= 2;
@@ -78,17 +78,27 @@ static int launch_small(const FbCall &c, int sms, unsigned *err, cudaStream_t st
 
 static int launch_large(const FbCall &c, int sms, unsigned *err, cudaStream_t st) {
   const bool gate = c.nmat == 2;
-  int rc = api_allow_smem(fb_large_kernel_fn(gate));
+  const int G = (c.K + FB_GROUP - 1) / FB_GROUP;
+  const long long tn = gate ? (c.N + 127) / 128 : (c.N + 255) / 256;
+  const long long singles = (c.M + 127LL) / 128 * tn, pairs = (c.M + 255LL) / 256 * tn;
+  // The form with fewer rounds of tiles over the SMs; pairs, which read a
+  // third less per product, where both need as many.
+  const bool pair = (singles + sms - 1) / sms >= (pairs + sms / 2 - 1) / (sms / 2) && pairs > sms / 4;
+  int ks = 1;
+  if (!pair)
+    while (ks < 8 && singles * ks * 2 <= sms && ks * 8 <= G) ks *= 2;
+  int rc = api_allow_smem(fb_large_kernel_fn(gate, pair));
   if (rc) return rc;
   FbMaps maps;
   memset(&maps, 0, sizeof maps);
   if ((rc = api_tensor_map_u8(c.qx, c.K, c.M, c.K, 128, 128, &maps.x))) return rc;
   for (int m = 0; m < c.nmat; ++m)
-    if ((rc = api_tensor_map_u8(c.qw[m], c.K, c.N, c.K, 128, 128, &maps.w[m]))) return rc;
+    if ((rc = api_tensor_map_u8(c.qw[m], c.K, c.N, c.K, 128, fb_large_weight_box(pair),
+                                &maps.w[m])))
+      return rc;
   const FbParams p{c.sx, {c.sw[0], c.sw[1]}, static_cast<uint16_t *>(c.y),
-                   static_cast<uint8_t *>(c.qh), c.sh, err, c.M, c.N,
-                   (c.K + FB_GROUP - 1) / FB_GROUP, 0};
-  const cudaError_t e = launch_fb_large(gate, maps, p, sms, st, api_pdl());
+                   static_cast<uint8_t *>(c.qh), c.sh, err, c.M, c.N, G, 0};
+  const cudaError_t e = launch_fb_large(gate, pair, ks, maps, p, sms, st, api_pdl());
   if (e != cudaSuccess) return api_cuda_error(e, "block-scaled FP8 product launch");
   return DFK_OK;
 }

@@ -30,20 +30,21 @@ constexpr int FBL_THREADS = 384;   // TMA, MMA and two scale warps; eight epilog
 // Registers a thread: 384 x 168 at launch, then 56 for the first warpgroup and
 // 224 for the two epilogue warpgroups (56 + 2 x 224 = 3 x 168).
 constexpr int FBL_REGS_IO = 56, FBL_REGS_EPI = 224;
-constexpr int FBL_STAGES = 6;
 constexpr int FBL_HALF = 128 * 128;           // bytes of one operand's half tile
-constexpr int FBL_STAGE = 2 * FBL_HALF;
+constexpr int FBL_RING = 12 * FBL_HALF;       // six stages of a pair, four of a single CTA
+constexpr int FBL_MAX_STAGES = 6;
+constexpr int FBL_PART_ROW = 1040;            // a token's 256 partial sums and 16 bytes
 constexpr int FBL_AHEAD = 8;       // groups whose scales are on the way (a power of two)
 constexpr int FBL_COMB = 4;        // groups whose s_x s_w are ready (a power of two)
 constexpr int FBL_BAND = 8;
 
-constexpr int FBL_OFF_OUT = FBL_STAGES * FBL_STAGE;        // 8 warps x 2 KB: output rows
+constexpr int FBL_OFF_OUT = FBL_RING;                      // 8 warps x 2 KB: output rows
 constexpr int FBL_OFF_SX = FBL_OFF_OUT + 8 * 2048;         // [AHEAD][128] s_x
 constexpr int FBL_OFF_SW = FBL_OFF_SX + FBL_AHEAD * 512;   // [AHEAD][2 warps][2] s_w
 constexpr int FBL_OFF_COMB = FBL_OFF_SW + FBL_AHEAD * 16;  // [COMB][2][128] s_x s_w
 constexpr int FBL_OFF_MAX = FBL_OFF_COMB + FBL_COMB * 1024;  // [2 tiles][2][128] row maxima
 constexpr int FBL_OFF_BAR = FBL_OFF_MAX + 2048;
-constexpr int FBL_BARS = 2 * FBL_STAGES + 13;
+constexpr int FBL_BARS = 2 * FBL_MAX_STAGES + 13;
 constexpr int FBL_SMEM = 1024 + FBL_OFF_BAR + FBL_BARS * 8 + 16;
 
 // ---- cta_group::2 forms
@@ -194,19 +195,15 @@ __device__ __forceinline__ void fbl_store_bf16(const FbParams &p, int m, int col
     if (col + e < p.N) at[e] = static_cast<uint16_t>(w[e >> 1] >> (16 * (e & 1)));
 }
 
-__device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
-  return f32_to_bf16_bits(lo) | (static_cast<uint32_t>(f32_to_bf16_bits(hi)) << 16);
-}
-
-template <bool GATE>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(FBL_THREADS, 1)
+template <bool GATE, bool PAIR>
+__global__ void __launch_bounds__(FBL_THREADS, 1)
     fb_large_kernel(const __grid_constant__ FbMaps maps, const FbParams p) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   const uint32_t raw_addr = smem_addr(smem_raw);
   uint8_t *smem = smem_raw + ((1024u - (raw_addr & 1023u)) & 1023u);
   const uint32_t sbase = smem_addr(smem);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  constexpr int S = FBL_STAGES;
+  constexpr int STAGE = (PAIR ? 2 : 3) * FBL_HALF, S = FBL_RING / STAGE;
 
   uint64_t *fullb = reinterpret_cast<uint64_t *>(smem + FBL_OFF_BAR);  // the leader's count
   uint64_t *empty = fullb + S;
@@ -219,10 +216,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(FBL_THREADS, 1)
   uint32_t *s_tmem = reinterpret_cast<uint32_t *>(done + 1) + 2;
 
   const uint32_t rank = cluster_rank();
-  const int pair = blockIdx.x >> 1, npairs = gridDim.x >> 1;
+  uint32_t csize;
+  asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(csize));
+  const int unit = blockIdx.x / csize, nunits = gridDim.x / csize;
+  // a single CTA's share of the groups (PAIR: all; its CTAs share the tokens)
+  const int ks = PAIR ? 1 : static_cast<int>(csize), kr = PAIR ? 0 : static_cast<int>(rank);
+  const int kb0 = static_cast<int>(static_cast<long long>(kr) * p.G / ks);
+  const int nkb = static_cast<int>(static_cast<long long>(kr + 1) * p.G / ks) - kb0;
+  constexpr int TM = PAIR ? 256 : 128;             // tokens of a tile
+  const int m_cta = PAIR ? static_cast<int>(rank) * 128 : 0;  // this CTA's first in it
+  const uint32_t lead = PAIR ? 0u : rank;          // the CTA that issues the MMAs
   const int NB = (p.N + 127) / 128;  // scale blocks along the weight rows
-  const FblTiles tiles{(p.M + 255) / 256, GATE ? NB : (p.N + 255) / 256};
+  const FblTiles tiles{(p.M + TM - 1) / TM, GATE ? NB : (p.N + 255) / 256};
   const int ntiles = tiles.count();
+  const int total = (ntiles - unit + nunits - 1) / nunits * nkb;  // groups of this CTA
 
   if (tid == 0) {
     for (int s = 0; s < S; ++s) {
@@ -231,7 +238,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(FBL_THREADS, 1)
     }
     for (int s = 0; s < 4; ++s) {
       mbar_init(&accfull[s], 3);   // the MMAs of a group's half and both scale warps
-      mbar_init(&accempty[s], 8);  // four epilogue warps of each CTA
+      mbar_init(&accempty[s], PAIR ? 8 : 4);  // four epilogue warps of each CTA
     }
     for (int s = 0; s < 4; ++s) mbar_init(&maxfull[s], 2);
     mbar_init(done, 1);
@@ -240,8 +247,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(FBL_THREADS, 1)
     fence_mbar_init();
   }
   if (warp == 1) {
-    tmem_alloc_pair(s_tmem, 512);
-    tmem_relinquish_pair();
+    if constexpr (PAIR) {
+      tmem_alloc_pair(s_tmem, 512);
+      tmem_relinquish_pair();
+    } else {
+      tmem_alloc(s_tmem, 512);
+      tmem_relinquish();
+    }
   }
   tc_fence_before();
   __syncthreads();
@@ -252,29 +264,45 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(FBL_THREADS, 1)
 
   if (warp < 4) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(FBL_REGS_IO));
   if (warp == 0) {
-    // ---- TMA: this CTA's 128 tokens and its 128 weight rows of every group
+    // ---- TMA: this CTA's 128 tokens and, of every group, its 128 weight rows
+    // (PAIR) or all 256: 64 rows of each half after the other
     if (lane == 0) {
       const uint64_t pol = l2_policy_evict_normal();
       pdl_wait();
-      int it = 0;
+      int it = 0, st = 0;
+      uint32_t ph = 0;
       bool ok = true;
-      for (int t = pair; ok && t < ntiles; t += npairs) {
+      for (int t = unit; ok && t < ntiles; t += nunits) {
         int tm, tn;
         tiles.at(t, tm, tn);
-        const int mrow = tm * 256 + static_cast<int>(rank) * 128;
-        const int wrow = GATE ? tn * 128 : tn * 256 + static_cast<int>(rank) * 128;
-        const CUtensorMap *wmap = GATE && rank ? &maps.w[1] : &maps.w[0];
-        for (int kb = 0; kb < p.G; ++kb, ++it) {
-          const int st = it % S;
-          if (it >= S && !fb_wait(&empty[st], ((it / S) - 1) & 1, s_abort, p.err)) {
+        const int mrow = tm * TM + m_cta;
+        for (int kb = kb0; kb < kb0 + nkb; ++kb, ++it) {
+          if (it >= S && !fb_wait(&empty[st], ph ^ 1u, s_abort, p.err)) {
             ok = false;
             break;
           }
-          if (rank == 0) mbar_arrive_expect_tx(&fullb[st], 2 * FBL_STAGE);
-          const uint32_t bar = cluster_map(smem_addr(&fullb[st]), 0);
-          uint8_t *sb = smem + st * FBL_STAGE;
-          tma_load_2d_pair(sb, &maps.x, bar, kb * 128, mrow, pol);
-          tma_load_2d_pair(sb + FBL_HALF, wmap, bar, kb * 128, wrow, pol);
+          uint8_t *sb = smem + st * STAGE;
+          if constexpr (PAIR) {
+            if (rank == 0) mbar_arrive_expect_tx(&fullb[st], 2 * STAGE);
+            const uint32_t bar = cluster_map(smem_addr(&fullb[st]), 0);
+            const CUtensorMap *wmap = GATE && rank ? &maps.w[1] : &maps.w[0];
+            const int wrow = GATE ? tn * 128 : tn * 256 + static_cast<int>(rank) * 128;
+            tma_load_2d_pair(sb, &maps.x, bar, kb * 128, mrow, pol);
+            tma_load_2d_pair(sb + FBL_HALF, wmap, bar, kb * 128, wrow, pol);
+          } else {
+            mbar_arrive_expect_tx(&fullb[st], STAGE);
+            tma_load_2d(sb, &maps.x, &fullb[st], kb * 128, mrow, pol);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {  // half i / 2, matrix or 128-row block i % 2
+              const int wrow = (GATE ? tn * 128 : tn * 256 + 128 * (i & 1)) + 64 * (i >> 1);
+              tma_load_2d(sb + FBL_HALF + i * (FBL_HALF / 2), &maps.w[GATE ? i & 1 : 0],
+                          &fullb[st], kb * 128, wrow, pol);
+            }
+          }
+          if (++st == S) {
+            st = 0;
+            ph ^= 1u;
+          }
         }
       }
       *s_issued = it;
@@ -284,47 +312,53 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(FBL_THREADS, 1)
     }
     __syncwarp();
   } else if (warp == 1) {
-    // ---- MMA, the leader CTA for both: 4 instructions of K = 32 per group
+    // ---- MMA (PAIR: CTA 0 for both): per half 4 instructions of K = 32
     const uint32_t leader = elect_one_sync();
-    if (rank == 0) {
-      const uint32_t idesc = umma_idesc_e4m3_f32(256, 128);
+    if (rank == lead) {
+      const uint32_t idesc = umma_idesc_e4m3_f32(PAIR ? 256 : 128, 128);
       const uint64_t desc0 = umma_desc_sw128(sbase);
-      int it = 0, st = 0;
+      // rows 64 h .. 64 h + 63 of both 128-row halves of the weights
+      constexpr uint32_t HALF_ENC = (PAIR ? FBL_HALF / 2 : FBL_HALF) >> 4;
+      auto commit = [&](uint64_t *bar) {
+        if constexpr (PAIR) umma_commit_pair(bar);
+        else umma_commit(bar);
+      };
+      int st = 0;
       uint32_t ph = 0;
-      bool ok = true;
-      for (int t = pair; ok && t < ntiles; t += npairs) {
-        for (int kb = 0; kb < p.G; ++kb, ++it) {
-          const int ab = it & 1;
-          ok = fb_wait(&fullb[st], ph, s_abort, p.err);
-          if (!__all_sync(0xffffffffu, ok)) break;
-          tc_fence_after();
-          const uint64_t da = desc0 + (static_cast<uint32_t>(st * FBL_STAGE) >> 4);
+      for (int it = 0; it < total; ++it) {
+        const int ab = it & 1;
+        bool ok = fb_wait(&fullb[st], ph, s_abort, p.err);
+        if (!__all_sync(0xffffffffu, ok)) break;
+        tc_fence_after();
+        const uint64_t da = desc0 + (static_cast<uint32_t>(st * STAGE) >> 4);
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            ok = it < 2 || fb_wait(&accempty[2 * ab + h], ((it >> 1) - 1) & 1, s_abort, p.err);
-            ok = __all_sync(0xffffffffu, ok);
-            if (!ok) break;
-            tc_fence_after();
-            // rows 64 h .. 64 h + 63 of each CTA's 128 weight rows
-            const uint64_t db = da + ((FBL_HALF + h * 64 * 128) >> 4);
-#pragma unroll
-            for (int kk = 0; kk < 4; ++kk)
-              if (leader)
-                umma_e4m3_pair(tmem + static_cast<uint32_t>(ab * 256 + h * 128), da + 2 * kk,
-                               db + 2 * kk, idesc, kk > 0 ? 1u : 0u);
-            if (leader) umma_commit_pair(&accfull[2 * ab + h]);
-            __syncwarp();
-          }
+        for (int h = 0; h < 2; ++h) {
+          ok = it < 2 || fb_wait(&accempty[2 * ab + h], ((it >> 1) - 1) & 1, s_abort, p.err);
+          ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
-          if (leader) umma_commit_pair(&empty[st]);
+          tc_fence_after();
+          const uint64_t db = da + (FBL_HALF >> 4) + h * HALF_ENC;
+          const uint32_t d = tmem + static_cast<uint32_t>(ab * 256 + h * 128);
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk)
+            if (leader) {
+              if constexpr (PAIR)
+                umma_e4m3_pair(d, da + 2 * kk, db + 2 * kk, idesc, kk > 0 ? 1u : 0u);
+              else
+                umma_e4m3(d, da + 2 * kk, db + 2 * kk, idesc, kk > 0 ? 1u : 0u);
+            }
+          if (leader) commit(&accfull[2 * ab + h]);
           __syncwarp();
-          if (++st == S) {
-            st = 0;
-            ph ^= 1u;
-          }
+        }
+        if (!ok) break;
+        if (leader) commit(&empty[st]);
+        __syncwarp();
+        if (++st == S) {
+          st = 0;
+          ph ^= 1u;
         }
       }
-      if (leader) umma_commit_pair(done);
+      if (leader) commit(done);
       __syncwarp();
     }
   } else if (warp < 4) {
@@ -337,13 +371,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(FBL_THREADS, 1)
     float *s_comb = reinterpret_cast<float *>(smem + FBL_OFF_COMB);
     const uint32_t sx_at = smem_addr(s_sx + row), sw_at = smem_addr(s_sw + lane);
     pdl_wait();  // s_x comes from the previous kernel
-    int ft = pair, fkb = 0, fn = 0;
+    int ft = unit, fkb = 0, fn = 0;
     const float *fx = nullptr, *fw = nullptr;
     bool in0 = false, in1 = false, inw = false;
     auto fetch_tile = [&]() {
       int tm = 0, tn = 0;
       if (ft < ntiles) tiles.at(ft, tm, tn);
-      const int m = tm * 256 + static_cast<int>(rank) * 128 + row;
+      const int m = tm * TM + m_cta + row;
       in0 = ft < ntiles && m < p.M;
       in1 = ft < ntiles && m + 32 < p.M;
       fx = p.sx + (in0 ? m : 0);
@@ -353,22 +387,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(FBL_THREADS, 1)
     };
     auto fetch = [&]() {
       const uint32_t slot = static_cast<uint32_t>(fn & (FBL_AHEAD - 1));
-      const float *x = fx + static_cast<size_t>(fkb) * p.M;
-      if (in0 && DFK_IN_BOUNDS(fkb < p.G, 32, p.err)) cp_async4(sx_at + slot * 512, x);
+      const float *x = fx + static_cast<size_t>(kb0 + fkb) * p.M;
+      if (in0 && DFK_IN_BOUNDS(kb0 + fkb < p.G, 32, p.err)) cp_async4(sx_at + slot * 512, x);
       if (in1) cp_async4(sx_at + slot * 512 + 128, x + 32);
-      if (inw) cp_async4(sw_at + slot * 16, fw + fkb);
+      if (inw) cp_async4(sw_at + slot * 16, fw + kb0 + fkb);
       cp_async_commit();
       ++fn;
-      if (++fkb == p.G) {
+      if (++fkb == nkb) {
         fkb = 0;
-        ft += npairs;
+        ft += nunits;
         fetch_tile();
       }
     };
     fetch_tile();
 #pragma unroll 1
     for (int i = 0; i < FBL_AHEAD - 1; ++i) fetch();
-    const int total = ((ntiles - pair + npairs - 1) / npairs) * p.G;
 #pragma unroll 1
     for (int it = 0; it < total; ++it) {
       const int slot = it & (FBL_AHEAD - 1), cs = it & (FBL_COMB - 1);
@@ -405,12 +438,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(FBL_THREADS, 1)
     const float *s_comb = reinterpret_cast<const float *>(smem + FBL_OFF_COMB) + row;
     float *s_max = reinterpret_cast<float *>(smem + FBL_OFF_MAX);
     uint8_t *obuf = smem + FBL_OFF_OUT + ew * 2048;
-    const uint32_t empty_at = cluster_map(smem_addr(&accempty[half]), 0);
+    const uint32_t empty_at = cluster_map(smem_addr(&accempty[half]), lead);
     pdl_wait();  // the outputs may still be read by the previous kernel
 
     int it = 0, nth = 0;
     bool ok = true, rdy = false;
-    for (int t = pair; ok && t < ntiles; t += npairs, ++nth) {
+    for (int t = unit; ok && t < ntiles; t += nunits, ++nth) {
       uint64_t acc[64];  // pairs of neighbouring columns
 #pragma unroll
       for (int i = 0; i < 64; ++i) acc[i] = 0ull;
@@ -418,7 +451,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(FBL_THREADS, 1)
       // next group's barrier is tested in the shadow of the last sums.
       const uint32_t tb = base + 128 * half;
 #pragma unroll 1
-      for (int kb = 0; kb < p.G; ++kb) {
+      for (int kb = 0; kb < nkb; ++kb) {
         const int ab = it & 1;
         if (!rdy) {
           ok = fb_wait(&accfull[2 * ab + half], (it >> 1) & 1, s_abort, p.err);
@@ -453,10 +486,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(FBL_THREADS, 1)
         }
       }
       if (!ok) break;
+      if (!PAIR && ks > 1) {
+        // ---- a share of a tile (each cluster has one): the partial sums go to
+        // shared memory, token by token, once every MMA has read the ring
+        ok = __all_sync(0xffffffffu, fb_wait(done, 0, s_abort, p.err));
+        if (!ok) break;
+        float *part = reinterpret_cast<float *>(smem + row * FBL_PART_ROW) + 64 * half;
+#pragma unroll
+        for (int i = 0; i < 64; i += 2) {
+          float4 v;
+          unpack_f32x2(acc[i], v.x, v.y);
+          unpack_f32x2(acc[i + 1], v.z, v.w);
+          *reinterpret_cast<float4 *>(part + (i < 32 ? 0 : 128) + 2 * (i & 31)) = v;
+        }
+        break;
+      }
       // ---- the tile's output
       int tm, tn;
       tiles.at(t, tm, tn);
-      const int m0 = tm * 256 + static_cast<int>(rank) * 128 + 32 * q;  // the warp's first row
+      const int m0 = tm * TM + m_cta + 32 * q;  // the warp's first row
       if constexpr (!GATE) {
         const int n0 = tn * 256 + 64 * half;
 #pragma unroll
@@ -525,17 +573,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(FBL_THREADS, 1)
     }
   }
 
-  // every wait above is bounded, so both CTAs come here; the MMAs have
-  // completed and both CTAs' copies have landed before either leaves
+  // every wait above is bounded, so all CTAs of the cluster come here; the MMAs
+  // have completed and the copies have landed before any leaves
   __syncthreads();
   if (tid == 0) {
     fb_wait(done, 0, nullptr, p.err);
     if (*s_abort) {
       const int issued = *s_issued;
-      if (rank == 0)
+      if (rank == lead)
         for (int i = max(0, issued - S); i < issued; ++i)
           fb_wait(&fullb[i % S], (i / S) & 1, nullptr, p.err);
-      // copies that only one of the CTAs issued are counted by no complete
+      // copies that only one CTA of a pair issued are counted by no complete
       // phase: they land within microseconds, allow a millisecond
       const unsigned long long t0 = global_timer_ns();
       for (int i = 0; i < 100000 && global_timer_ns() - t0 < 1000000ull; ++i) __nanosleep(1000);
@@ -544,24 +592,72 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(FBL_THREADS, 1)
   __syncthreads();
   cluster_sync_all();
   tc_fence_after();
-  if (warp == 1) tmem_dealloc_pair(tmem, 512);
+  if (warp == 1) {
+    if constexpr (PAIR) tmem_dealloc_pair(tmem, 512);
+    else tmem_dealloc(tmem, 512);
+  }
+  if (!PAIR && ks > 1) {
+    // ---- the cluster's shares added in rank order through distributed shared
+    // memory: a token per warp and turn, spread over the CTAs
+    if (warp >= 4 && !*s_abort) {
+      int tm, tn;
+      tiles.at(unit, tm, tn);
+      const int nt = min(128, p.M - tm * 128);
+      for (int n = kr * 8 + (warp - 4); n < nt; n += 8 * ks) {
+        float a[2][4];
+#pragma unroll
+        for (int b = 0; b < 2; ++b) {
+          const uint32_t at = sbase + static_cast<uint32_t>(n * FBL_PART_ROW + 512 * b + 16 * lane);
+          float4 t = ld_cluster_f4(cluster_map(at, 0));
+          for (int r = 1; r < ks; ++r) {
+            const float4 o = ld_cluster_f4(cluster_map(at, r));
+            t.x += o.x;
+            t.y += o.y;
+            t.z += o.z;
+            t.w += o.w;
+          }
+          a[b][0] = t.x;
+          a[b][1] = t.y;
+          a[b][2] = t.z;
+          a[b][3] = t.w;
+        }
+        if constexpr (GATE) {
+          fb_emit4<2>(p, tm * 128 + n, tn, lane, a);
+        } else {
+#pragma unroll
+          for (int b = 0; b < 2; ++b) {
+            const float v[1][4] = {{a[b][0], a[b][1], a[b][2], a[b][3]}};
+            fb_emit4<1>(p, tm * 128 + n, 2 * tn + b, lane, v);
+          }
+        }
+      }
+    }
+    __syncwarp();
+    cluster_sync_all();  // no CTA leaves while its sums are being read
+  }
 }
 
-cudaError_t launch_fb_large(bool gate, const FbMaps &maps, const FbParams &p, int sms,
-                            cudaStream_t st, bool pdl) {
-  const void *fn = fb_large_kernel_fn(gate);
-  const long long tm = (p.M + 255) / 256, tn = gate ? (p.N + 127) / 128 : (p.N + 255) / 256;
-  const long long pairs = std::min<long long>(sms / 2, tm * tn);
+const void *fb_large_kernel_fn(bool gate, bool pair) {
+  return gate ? (pair ? reinterpret_cast<const void *>(&fb_large_kernel<true, true>)
+                      : reinterpret_cast<const void *>(&fb_large_kernel<true, false>))
+              : (pair ? reinterpret_cast<const void *>(&fb_large_kernel<false, true>)
+                      : reinterpret_cast<const void *>(&fb_large_kernel<false, false>));
+}
+
+int fb_large_weight_box(bool pair) { return pair ? 128 : 64; }
+
+cudaError_t launch_fb_large(bool gate, bool pair, int ks, const FbMaps &maps, const FbParams &p,
+                            int sms, cudaStream_t st, bool pdl) {
+  const int tokens = pair ? 256 : 128, cluster = pair ? 2 : ks;
+  const long long tm = (p.M + tokens - 1) / tokens;
+  const long long tn = gate ? (p.N + 127) / 128 : (p.N + 255) / 256;
+  const long long units = ks > 1 ? tm * tn : std::min<long long>(sms / cluster, tm * tn);
   FbMaps mp = maps;
   FbParams pp = p;
   void *args[] = {&mp, &pp};
-  return launch_kernel(fn, dim3(static_cast<unsigned>(2 * pairs)), dim3(FBL_THREADS), FBL_SMEM,
-                       st, pdl, args);
-}
-
-const void *fb_large_kernel_fn(bool gate) {
-  return gate ? reinterpret_cast<const void *>(&fb_large_kernel<true>)
-              : reinterpret_cast<const void *>(&fb_large_kernel<false>);
+  return launch_kernel(fb_large_kernel_fn(gate, pair), dim3(static_cast<unsigned>(cluster * units)),
+                       dim3(FBL_THREADS), FBL_SMEM, st, pdl, args,
+                       static_cast<unsigned>(cluster));
 }
 
 }  // namespace dfk

@@ -319,34 +319,7 @@ __global__ void __launch_bounds__(FbsShape<NMAT, BN>::threads)
         a[m][2] = t.z;
         a[m][3] = t.w;
       }
-      const int j = j0 + 4 * lane;
-      float h[4];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        if (NMAT == 2) h[e] = fb_silu_mul(a[0][e], a[NMAT - 1][e]);
-        else h[e] = a[0][e];
-        if (j + e >= p.N) h[e] = 0.f;
-      }
-      const size_t at = static_cast<size_t>(n0 + n) * p.N + j;
-      if (NMAT == 2 && p.y == nullptr) {
-        float mx = max_nan(max_nan(fabsf(h[0]), fabsf(h[1])), max_nan(fabsf(h[2]), fabsf(h[3])));
-#pragma unroll
-        for (int d = 16; d >= 1; d >>= 1) mx = max_nan(mx, __shfl_xor_sync(0xffffffffu, mx, d));
-        const FbScale f = fb_scale(mx);
-        if (j < p.N && DFK_IN_BOUNDS(j + 4 <= p.N && n0 + n < p.M, 28, p.err))
-          *reinterpret_cast<uint32_t *>(p.qh + at) = fb_codes4(h[0], h[1], h[2], h[3], f);
-        if (lane == 0) p.sh[static_cast<size_t>(blk) * p.M + n0 + n] = f.s;
-      } else if ((p.N & 3) == 0) {
-        if (j < p.N && DFK_IN_BOUNDS(j + 4 <= p.N && n0 + n < p.M, 29, p.err))
-          *reinterpret_cast<uint2 *>(p.y + at) =
-              make_uint2(f32_to_bf16_bits(h[0]) | (static_cast<uint32_t>(f32_to_bf16_bits(h[1])) << 16),
-                         f32_to_bf16_bits(h[2]) | (static_cast<uint32_t>(f32_to_bf16_bits(h[3])) << 16));
-      } else {
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          if (j + e < p.N && DFK_IN_BOUNDS(n0 + n < p.M, 30, p.err))
-            p.y[at + e] = f32_to_bf16_bits(h[e]);
-      }
+      fb_emit4<NMAT>(p, n0 + n, blk, lane, a);
     }
   }
   __syncwarp();
@@ -360,15 +333,11 @@ static int smem_of(int stages) {
   return 1024 + ring + Sh::comb_floats * 4 + (2 * stages + 5) * 8 + 16;
 }
 
-#define DFK_FBS_PICK(expr)               \
-  (nmat == 1 ? (bn == 16    ? expr(1, 16)  \
-                : bn == 32  ? expr(1, 32)  \
-                : bn == 64  ? expr(1, 64)  \
-                            : expr(1, 128)) \
-             : (bn == 16    ? expr(2, 16)  \
-                : bn == 32  ? expr(2, 32)  \
-                : bn == 64  ? expr(2, 64)  \
-                            : expr(2, 128)))
+#define DFK_FBS_PICK(expr)                             \
+  (nmat == 1 ? (bn == 16   ? expr(1, 16)                \
+                : bn == 32 ? expr(1, 32) : expr(1, 64)) \
+             : (bn == 16   ? expr(2, 16)                \
+                : bn == 32 ? expr(2, 32) : expr(2, 64)))
 
 const void *fb_small_kernel(int nmat, int bn) {
 #define DFK_FBS_FN(NM, B) reinterpret_cast<const void *>(&fb_small_kernel_t<NM, B>)

@@ -218,7 +218,7 @@ SHAPES = [(1, 16, 1), (1, 128, 128), (2, 144, 130), (1, 4096, 512), (3, 2064, 10
           (16, 1040, 129), (17, 256, 688), (31, 688, 256), (33, 272, 96), (64, 512, 4096),
           (65, 512, 1032), (127, 640, 384), (128, 128, 257), (129, 1152, 640), (200, 400, 1000),
           (255, 2064, 255), (256, 256, 256), (257, 384, 520), (300, 14336, 200), (513, 144, 768),
-          (777, 2064, 1001), (1024, 1024, 1024)]
+          (777, 2064, 1001), (1024, 1024, 1024), (1100, 400, 5000), (2500, 144, 2056)]
 
 
 @pytest.mark.parametrize("M,K,N", SHAPES)
