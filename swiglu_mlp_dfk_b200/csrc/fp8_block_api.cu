@@ -24,9 +24,6 @@ static int check_rows(int M, int K) {
 constexpr int FB_SMEM_MAX = 232448;     // bytes a CTA may use
 constexpr int FB_SMEM_HALF = 115712;    // two CTAs on an SM
 
-// Up to this many tokens a product streams its weights (fp8_block_small.cu).
-constexpr int FB_SMALL_MAX_M = 64;
-
 struct FbCall {
   int nmat;
   const void *qx;
@@ -38,67 +35,105 @@ struct FbCall {
   int M, K, N;
 };
 
-static int launch_small(const FbCall &c, int sms, unsigned *err, cudaStream_t st) {
-  const int G = (c.K + FB_GROUP - 1) / FB_GROUP;
-  const int bn = c.M <= 16 ? 16 : c.M <= 32 ? 32 : 64;
-  const int blocks = (c.N + 127) / 128, tiles = (c.M + bn - 1) / bn;
-  if (tiles > 65535) return api_fail(DFK_ERR_UNSUPPORTED_SHAPE, "M=%d is too large", c.M);
-  // Clusters of 1, 2, 4 or 8 CTAs a row block, each with four groups or more.
-  // One matrix: up to two CTAs on an SM, so that the next call's weights load
-  // while this one ends (N = 6144, K = 4096: 7.3 us against 9.1 at one CTA;
-  // clusters of 3, as many as fill the SMs, 15.5: they do not all fit at once).
-  // Two matrices: one CTA on an SM with all of its shared memory (stages of
-  // 32 KB and more), two where the row blocks outnumber the SMs.
-  const long long work = static_cast<long long>(blocks) * tiles;
-  const bool pack = c.nmat == 1 || (bn < 64 && work > sms);
-  const int limit = pack ? 2 * sms : sms;
-  int ks = 1;
-  while (ks < 8 && work * ks * 2 <= limit && ks * 8 <= G) ks *= 2;
-  const int cap = pack ? FB_SMEM_HALF : FB_SMEM_MAX;
-  int stages = fb_small_min_stages(c.nmat, bn);
-  const int most = (G + ks - 1) / ks;
-  while (stages < 16 && stages < most && fb_small_smem(c.nmat, bn, stages + 1) <= cap) ++stages;
-  const void *fn = fb_small_kernel(c.nmat, bn);
+// ---- which kernel, in which form
+
+static int ceil_div(long long a, long long b) { return static_cast<int>((a + b - 1) / b); }
+
+// The streaming kernel (fp8_block_small.cu): tokens of a tile, CTAs of a row block,
+// two CTAs on an SM or one.  Clusters of 1, 2, 4 or 8 CTAs a row block, each with
+// four groups or more.  One matrix: two CTAs on an SM, so that the next call's
+// weights load while this one ends (16 tokens, N = 6144, K = 4096: 7.3 us against
+// 9.1 at one CTA; clusters of 3, as many as fill the SMs, 15.5: they do not all
+// fit at once).  Two matrices: one CTA on an SM with all of its shared memory
+// (stages of 32 KB and more), two where the row blocks outnumber the SMs.
+struct SmallPlan {
+  int bn, blocks, tiles, ks;
+  bool pack;
+  double us;
+};
+
+static SmallPlan plan_small(const FbCall &c, int G, int sms) {
+  SmallPlan s;
+  s.bn = c.M <= 16 ? 16 : c.M <= 32 ? 32 : 64;
+  s.blocks = ceil_div(c.N, 128);
+  s.tiles = ceil_div(c.M, s.bn);
+  const long long work = static_cast<long long>(s.blocks) * s.tiles;
+  s.pack = c.nmat == 1 || (s.bn < 64 && work > sms);
+  const int limit = s.pack ? 2 * sms : sms;
+  s.ks = 1;
+  while (s.ks < 8 && work * s.ks * 2 <= limit && s.ks * 8 <= G) s.ks *= 2;
+  s.us = 5.0 + 0.57 * ceil_div(G, s.ks) * ceil_div(work * s.ks, limit);
+  return s;
+}
+
+// The tensor-bound kernel (fp8_block_large.cu): tiles of 256 tokens by pairs of
+// CTAs, or of 128 tokens by single CTAs or clusters of ks of them.  Clusters of
+// 8 do not all fit on the SMs (96 tokens, N = 4096, K = 14336: 34 us, 22 with 4).
+struct LargePlan {
+  bool pair;
+  int ks;
+  double us;
+};
+
+static LargePlan plan_large(const FbCall &c, int G, int sms) {
+  const long long tn = ceil_div(c.N, c.nmat == 2 ? 128 : 256);
+  const long long singles = ceil_div(c.M, 128) * tn, pairs = ceil_div(c.M, 256) * tn;
+  LargePlan best{true, 1, 6.0 + 0.36 * G * ceil_div(pairs, sms / 2)};
+  for (int ks = 1; ks <= 4 && ks * 4 <= std::max(G, 4); ks *= 2) {
+    if (ks > 1 && singles * ks > sms * 9 / 10) break;
+    const double us =
+        (ks > 1 ? 10.0 : 6.0) + 0.42 * ceil_div(G, ks) * ceil_div(singles * ks, sms);
+    if (us < best.us) best = LargePlan{false, ks, us};
+  }
+  return best;
+}
+
+// `us` above: what a call takes, fitted to 30 shapes of 48 to 4096 tokens on a
+// B200: a fixed part (launch, first loads, output; 4 us more where a cluster adds
+// its shares) and a part per group and round of tiles.  Both sides at 192 tokens:
+// N = 6144, K = 4096 15.5 us streaming, 17.9 by pairs; N = 4096, K = 14336 36 us
+// streaming, 24 by clusters of 4, 47 by pairs; N = 16384, K = 4096 41, 21.5, 20.
+static int launch_small(const FbCall &c, const SmallPlan &s, int G, unsigned *err,
+                        cudaStream_t st) {
+  if (s.tiles > 65535) return api_fail(DFK_ERR_UNSUPPORTED_SHAPE, "M=%d is too large", c.M);
+  const int cap = s.pack ? FB_SMEM_HALF : FB_SMEM_MAX;
+  int stages = fb_small_min_stages(c.nmat, s.bn);
+  const int most = ceil_div(G, s.ks);
+  while (stages < 16 && stages < most && fb_small_smem(c.nmat, s.bn, stages + 1) <= cap) ++stages;
+  const void *fn = fb_small_kernel(c.nmat, s.bn);
   int rc = api_allow_smem(fn);
   if (rc) return rc;
   FbMaps maps;
   memset(&maps, 0, sizeof maps);
-  if ((rc = api_tensor_map_u8(c.qx, c.K, c.M, c.K, 128, bn, &maps.x))) return rc;
+  if ((rc = api_tensor_map_u8(c.qx, c.K, c.M, c.K, 128, s.bn, &maps.x))) return rc;
   for (int m = 0; m < c.nmat; ++m)
     if ((rc = api_tensor_map_u8(c.qw[m], c.K, c.N, c.K, 128, 128, &maps.w[m]))) return rc;
   FbParams p{c.sx, {c.sw[0], c.sw[1]}, static_cast<uint16_t *>(c.y),
              static_cast<uint8_t *>(c.qh), c.sh, err, c.M, c.N, G, stages};
   void *args[] = {&maps, &p};
   const cudaError_t e = launch_kernel(
-      fn, dim3(static_cast<unsigned>(blocks * ks), tiles), dim3(fb_small_threads(c.nmat, bn)),
-      fb_small_smem(c.nmat, bn, stages), st, api_pdl(), args, static_cast<unsigned>(ks));
+      fn, dim3(static_cast<unsigned>(s.blocks) * s.ks, s.tiles),
+      dim3(fb_small_threads(c.nmat, s.bn)), fb_small_smem(c.nmat, s.bn, stages), st, api_pdl(),
+      args, static_cast<unsigned>(s.ks));
   if (e != cudaSuccess) return api_cuda_error(e, "block-scaled FP8 product launch");
   return DFK_OK;
 }
 
-static int launch_large(const FbCall &c, int sms, unsigned *err, cudaStream_t st) {
+static int launch_large(const FbCall &c, const LargePlan &l, int G, int sms, unsigned *err,
+                        cudaStream_t st) {
   const bool gate = c.nmat == 2;
-  const int G = (c.K + FB_GROUP - 1) / FB_GROUP;
-  const long long tn = gate ? (c.N + 127) / 128 : (c.N + 255) / 256;
-  const long long singles = (c.M + 127LL) / 128 * tn, pairs = (c.M + 255LL) / 256 * tn;
-  // The form with fewer rounds of tiles over the SMs; pairs, which read a
-  // third less per product, where both need as many.
-  const bool pair = (singles + sms - 1) / sms >= (pairs + sms / 2 - 1) / (sms / 2) && pairs > sms / 4;
-  int ks = 1;
-  if (!pair)
-    while (ks < 8 && singles * ks * 2 <= sms && ks * 8 <= G) ks *= 2;
-  int rc = api_allow_smem(fb_large_kernel_fn(gate, pair));
+  int rc = api_allow_smem(fb_large_kernel_fn(gate, l.pair));
   if (rc) return rc;
   FbMaps maps;
   memset(&maps, 0, sizeof maps);
   if ((rc = api_tensor_map_u8(c.qx, c.K, c.M, c.K, 128, 128, &maps.x))) return rc;
   for (int m = 0; m < c.nmat; ++m)
-    if ((rc = api_tensor_map_u8(c.qw[m], c.K, c.N, c.K, 128, fb_large_weight_box(pair),
+    if ((rc = api_tensor_map_u8(c.qw[m], c.K, c.N, c.K, 128, fb_large_weight_box(l.pair),
                                 &maps.w[m])))
       return rc;
   const FbParams p{c.sx, {c.sw[0], c.sw[1]}, static_cast<uint16_t *>(c.y),
                    static_cast<uint8_t *>(c.qh), c.sh, err, c.M, c.N, G, 0};
-  const cudaError_t e = launch_fb_large(gate, pair, ks, maps, p, sms, st, api_pdl());
+  const cudaError_t e = launch_fb_large(gate, l.pair, l.ks, maps, p, sms, st, api_pdl());
   if (e != cudaSuccess) return api_cuda_error(e, "block-scaled FP8 product launch");
   return DFK_OK;
 }
@@ -130,7 +165,13 @@ static int product(const FbCall &c, cudaStream_t st) {
   int sms;
   unsigned *err;
   if ((rc = api_device(&sms, &err))) return rc;
-  return c.M <= FB_SMALL_MAX_M ? launch_small(c, sms, err, st) : launch_large(c, sms, err, st);
+  // up to 64 tokens the weights' bytes bound every form: the streaming kernel
+  const int G = ceil_div(c.K, FB_GROUP);
+  const SmallPlan small = plan_small(c, G, sms);
+  if (c.M <= 64) return launch_small(c, small, G, err, st);
+  const LargePlan large = plan_large(c, G, sms);
+  return small.us <= large.us ? launch_small(c, small, G, err, st)
+                              : launch_large(c, large, G, sms, err, st);
 }
 
 }  // namespace dfk
