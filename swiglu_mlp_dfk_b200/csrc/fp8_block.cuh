@@ -142,6 +142,34 @@ __device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr) {
   return v;
 }
 
+// The cluster's shares of a token's sums (NV values of four columns, `vstep`
+// bytes apart) added in rank order; at: this CTA's address of the first, the
+// same in every CTA.  Four ranks' loads are on their way together.
+template <int NV>
+__device__ __forceinline__ void fb_sum_shares(uint32_t at, uint32_t vstep, int ks,
+                                              float4 (&sum)[NV]) {
+#pragma unroll
+  for (int v = 0; v < NV; ++v) sum[v] = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int r0 = 0; r0 < ks; r0 += 4) {
+    float4 o[4][NV];
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+#pragma unroll
+      for (int v = 0; v < NV; ++v)
+        o[r][v] = ld_cluster_f4(cluster_map(at + v * vstep, min(r0 + r, ks - 1)));
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+#pragma unroll
+      for (int v = 0; v < NV; ++v)
+        if (r0 + r < ks) {
+          sum[v].x += o[r][v].x;
+          sum[v].y += o[r][v].y;
+          sum[v].z += o[r][v].z;
+          sum[v].w += o[r][v].w;
+        }
+  }
+}
+
 __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
   return f32_to_bf16_bits(lo) | (static_cast<uint32_t>(f32_to_bf16_bits(hi)) << 16);
 }
@@ -168,12 +196,13 @@ struct FbParams {
 // rows a lane: bf16, or codes and the group's scale.
 template <int NMAT>
 __device__ __forceinline__ void fb_emit4(const FbParams &p, int m, int blk, int lane,
-                                         const float (&a)[NMAT][4]) {
+                                         const float4 &a, const float4 &up) {
   const int j = blk * 128 + 4 * lane;
-  float h[4];
+  float h[4] = {a.x, a.y, a.z, a.w};
+  const float u[4] = {up.x, up.y, up.z, up.w};
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
-    h[e] = NMAT == 2 ? fb_silu_mul(a[0][e], a[NMAT - 1][e]) : a[0][e];
+    if (NMAT == 2) h[e] = fb_silu_mul(h[e], u[e]);
     if (j + e >= p.N) h[e] = 0.f;
   }
   const size_t at = static_cast<size_t>(m) * p.N + j;

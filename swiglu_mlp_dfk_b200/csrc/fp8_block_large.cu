@@ -604,31 +604,14 @@ __global__ void __launch_bounds__(FBL_THREADS, 1)
       tiles.at(unit, tm, tn);
       const int nt = min(128, p.M - tm * 128);
       for (int n = kr * 8 + (warp - 4); n < nt; n += 8 * ks) {
-        float a[2][4];
-#pragma unroll
-        for (int b = 0; b < 2; ++b) {
-          const uint32_t at = sbase + static_cast<uint32_t>(n * FBL_PART_ROW + 512 * b + 16 * lane);
-          float4 t = ld_cluster_f4(cluster_map(at, 0));
-          for (int r = 1; r < ks; ++r) {
-            const float4 o = ld_cluster_f4(cluster_map(at, r));
-            t.x += o.x;
-            t.y += o.y;
-            t.z += o.z;
-            t.w += o.w;
-          }
-          a[b][0] = t.x;
-          a[b][1] = t.y;
-          a[b][2] = t.z;
-          a[b][3] = t.w;
-        }
+        float4 a[2];
+        fb_sum_shares<2>(sbase + static_cast<uint32_t>(n * FBL_PART_ROW + 16 * lane), 512, ks, a);
+        const int m = tm * 128 + n;
         if constexpr (GATE) {
-          fb_emit4<2>(p, tm * 128 + n, tn, lane, a);
+          fb_emit4<2>(p, m, tn, lane, a[0], a[1]);
         } else {
-#pragma unroll
-          for (int b = 0; b < 2; ++b) {
-            const float v[1][4] = {{a[b][0], a[b][1], a[b][2], a[b][3]}};
-            fb_emit4<1>(p, tm * 128 + n, 2 * tn + b, lane, v);
-          }
+          fb_emit4<1>(p, m, 2 * tn, lane, a[0], a[0]);
+          fb_emit4<1>(p, m, 2 * tn + 1, lane, a[1], a[1]);
         }
       }
     }

@@ -301,25 +301,29 @@ __global__ void __launch_bounds__(FbsShape<NMAT, BN>::threads)
     // one token per warp and turn, spread over the cluster's CTAs; lane l
     // takes rows 4 l .. 4 l + 3
     const int nt = min(BN, p.M - n0);
-    for (int n = rank * Sh::warps + (warp - 2); n < nt; n += Sh::warps * ks) {
-      float a[NMAT][4];
+    if (ks == 1) {
+      // four tokens' sums in registers at a time: one after the other, a round
+      // trip each, cost up to 2 us
+      for (int n = warp - 2; n < nt; n += 4 * Sh::warps) {
+        float4 a[4][NMAT];
 #pragma unroll
-      for (int m = 0; m < NMAT; ++m) {
-        const uint32_t at = sbase + static_cast<uint32_t>(((m * BN + n) * 128 + 4 * lane) * 4);
-        float4 t = ld_cluster_f4(cluster_map(at, 0));
-        for (uint32_t r = 1; r < ks; ++r) {
-          const float4 o = ld_cluster_f4(cluster_map(at, r));
-          t.x += o.x;
-          t.y += o.y;
-          t.z += o.z;
-          t.w += o.w;
-        }
-        a[m][0] = t.x;
-        a[m][1] = t.y;
-        a[m][2] = t.z;
-        a[m][3] = t.w;
+        for (int u = 0; u < 4; ++u)
+#pragma unroll
+          for (int m = 0; m < NMAT; ++m)
+            a[u][m] = *reinterpret_cast<const float4 *>(
+                smem + ((m * BN + min(n + u * Sh::warps, BN - 1)) * 128 + 4 * lane) * 4);
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+          if (n + u * Sh::warps < nt)
+            fb_emit4<NMAT>(p, n0 + n + u * Sh::warps, blk, lane, a[u][0], a[u][NMAT - 1]);
       }
-      fb_emit4<NMAT>(p, n0 + n, blk, lane, a);
+    } else {
+      for (int n = rank * Sh::warps + (warp - 2); n < nt; n += Sh::warps * ks) {
+        float4 a[NMAT];
+        fb_sum_shares<NMAT>(sbase + static_cast<uint32_t>((n * 128 + 4 * lane) * 4), BN * 512, ks,
+                            a);
+        fb_emit4<NMAT>(p, n0 + n, blk, lane, a[0], a[NMAT - 1]);
+      }
     }
   }
   __syncwarp();
