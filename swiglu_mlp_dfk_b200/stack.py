@@ -22,7 +22,11 @@ The unfused variant runs the same step with separate kernels (RMSNorm, two
 GEMVs, SiLU, multiply, down projection) and bf16 intermediates in HBM.  The
 FP8 variant encodes every layer's weights once as E4M3 codes with one fp32
 scale per output row (the library's FP8 entry points: half the weight bytes
-per step, dequantised inside the kernels).
+per step, dequantised inside the kernels).  The block-scaled FP8 variant
+(``fp8="block"``) keeps the activations in 8 bits as well, with one scale per
+token and group of 128 and per 128 x 128 weight block: RMSNorm into codes, the
+gate/up kernel from codes to codes, the down product from codes; it takes any
+number of tokens, a prompt's as well as a decode batch.
 
 In-context tuning (``tune_variants``): the library's scheduler times each
 operation on its own, in bursts of back-to-back launches of that one
@@ -54,6 +58,8 @@ class DecodeStack:
     layout: "row", "col", "interleaved" or "auto" -- how the fused bf16
             stack stores W_gate / W_up (converted copies; "auto" asks the
             scheduler); the unfused and FP8 stacks are row-major only
+    fp8:    False, True (codes with row scales) or "block" (block-scaled
+            weights and activations; any number of tokens)
     """
 
     def __init__(self, layers, x0, eps=1e-5, fused=True, fp8=False, layout="row"):
@@ -65,8 +71,15 @@ class DecodeStack:
             raise ValueError("only the fused bf16 stack takes another weight layout")
         self.eps = float(eps)
         self.fused = fused
-        self.fp8 = fp8
-        if fp8:
+        if fp8 not in (False, True, "block"):
+            raise ValueError("fp8 must be False, True or \"block\"")
+        self.fp8 = bool(fp8)
+        self.block = fp8 == "block"
+        if self.block:
+            from . import inputs as I
+            layers = [(gamma,) + I.to_fp8_blocks(wg) + I.to_fp8_blocks(wu) + I.to_fp8_blocks(wd)
+                      for gamma, wg, wu, wd in layers]
+        elif fp8:
             from . import inputs as I
             enc = []
             for gamma, wg, wu, wd in layers:
@@ -96,7 +109,14 @@ class DecodeStack:
         self.x = x0.clone()                       # step input (graph-static buffer)
         self.acts = [torch.empty(self.B, self.D, dtype=torch.bfloat16, device=dev)
                      for _ in range(2)]          # ping-pong layer outputs
-        self.h = torch.empty(self.B, self.F, dtype=torch.bfloat16, device=dev)
+        if self.block:
+            def codes(n):
+                return (torch.empty(self.B, n, dtype=torch.float8_e4m3fn, device=dev),
+                        torch.empty(-(-n // 128), self.B, dtype=torch.float32, device=dev))
+            self.xn = codes(self.D)                # codes and scales of the normed input
+            self.h = codes(self.F)                 # and of h
+        else:
+            self.h = torch.empty(self.B, self.F, dtype=torch.bfloat16, device=dev)
         if not fused:
             self.xn = torch.empty(self.B, self.D, dtype=torch.bfloat16, device=dev)
             self.a = torch.empty_like(self.h)
@@ -116,6 +136,13 @@ class DecodeStack:
     def _layer(self, l):
         xin = self.layer_input(l)
         y = self.acts[l % 2]
+        if self.block:
+            gamma, qg, sg, qu, su, qd, sd = self.layers[l]
+            q, s = self.xn
+            dfk.dfk_add_rmsnorm_fp8_block(xin, None, gamma, self.eps, q=q, s=s)
+            dfk.dfk_swiglu_gate_up_fp8_block(q, s, qg, sg, qu, su, q_h=self.h[0], s_h=self.h[1])
+            dfk.dfk_gemm_fp8_block(*self.h, qd, sd, y=y)
+            return
         if self.fp8:
             gamma, qg, sg, qu, su, qd, sd = self.layers[l]
             dfk.dfk_rmsnorm_swiglu_gate_up_fp8(xin, gamma, self.eps, qg, sg, qu, su, h=self.h,
@@ -223,6 +250,8 @@ class DecodeStack:
         library's choice."""
         if not self.fused:
             raise ValueError("in-context tuning covers the fused stacks")
+        if self.block:
+            raise ValueError("the block-scaled kernels have no variants to choose from")
         self.gu_variant = self.dn_variant = 0
         base = self._time_step(steps)
         best = base
@@ -242,11 +271,16 @@ class DecodeStack:
     def kernels_per_step(self):
         """Library calls per step (one kernel each, except the FP8 tensor-core
         calls that launch a prep kernel first)."""
-        return len(self.layers) * (2 if self.fused else 6) + 1
+        return len(self.layers) * (3 if self.block else 2 if self.fused else 6) + 1
 
     def bytes_per_step(self):
         """Algorithmic bytes of one step: every weight once, activations in/out."""
         B, D, F = self.B, self.D, self.F
+        if self.block:
+            g_d, g_f = -(-D // 128), -(-F // 128)
+            weights = 3 * F * D + 3 * 4 * g_d * g_f
+            codes = 2 * B * (D + F) + 2 * 4 * B * (g_d + g_f)       # written, then read
+            return len(self.layers) * (weights + codes + 4 * B * D + 2 * D) + 2 * B * D * 2
         if self.fp8:  # codes (1 byte) + fp32 row scales
             per_layer = (2 * F * D + 2 * F * 4 + B * D * 2 + D * 2 + B * F * 2
                          + D * F + D * 4 + B * F * 2 + B * D * 2)

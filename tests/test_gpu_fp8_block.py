@@ -415,6 +415,38 @@ def test_layer_in_a_graph_and_on_two_streams(M):
     assert all(same(o, l(*x)) for o, l, x in zip(outs, layers, xs))
 
 
+@pytest.mark.parametrize("B", [4, 100])
+def test_decode_stack_in_block_scaled_fp8(B):
+    from swiglu_mlp_dfk_b200.stack import DecodeStack
+    x0, params = I.make_stack(3, B, 512, 1040, seed=B, w_std=0.05)
+    st, ref = (DecodeStack(params, x0, fp8="block") for _ in range(2))
+    st.step()
+    ref.step_eager()
+    st.capture()
+    for _ in range(3):
+        st.step()
+        ref.step_eager()
+        torch.cuda.synchronize()
+        assert torch.equal(st.x, ref.x)
+    for l in range(3):                     # one layer at a time, on its own input
+        x = ref.layer_input(l).clone()
+        with torch.cuda.stream(ref.stream):
+            ref._layer(l)
+        torch.cuda.synchronize()
+        gamma, qg, sg, qu, su, qd, sd = ref.layers[l]
+        d = x.double()
+        v = d / (d.square().mean(1, keepdim=True) + ref.eps).sqrt() * gamma.double()
+        check_quantised(*ref.xn, v, 2.0 ** -18 * v.abs())
+        h, eh = silu_mul(*product(*ref.xn, qg, sg), *product(*ref.xn, qu, su))
+        check_quantised(*ref.h, h, eh)
+        check_rounded(ref.acts[l % 2], *product(*ref.h, qd, sd), 2.0 ** -8)
+    with pytest.raises(ValueError):
+        st.tune_variants()
+    with pytest.raises(ValueError):
+        DecodeStack(params, x0, fp8="rows")
+    assert st.kernels_per_step() == 10 and st.bytes_per_step() > 3 * 3 * 512 * 1040
+
+
 def test_large_offsets():
     """Outputs whose offsets pass 32 bits: 70,000 tokens x 32,000 columns of bf16 (4.5 GB)."""
     M, K, N = 70000, 128, 32000
