@@ -24,9 +24,9 @@ constexpr int FBS_PRE = 4;         // groups whose scales are loaded ahead
 template <int NMAT, int BN>
 struct FbsShape {
   // epilogue warps: one for each TMEM lane quarter, two where four would have
-  // more than 64 sums a thread (64 tokens of a gated product: 27 us with four
-  // warps, 32 columns of each matrix every 60 cycles, against 21 with eight)
-  static constexpr int warps = NMAT * BN > 64 ? 8 : 4;
+  // 64 sums a thread or more (4096 x 14336 gated: 64 tokens 27.3 us with four,
+  // 23.5 with eight; 32 tokens 22.8 and 22.0)
+  static constexpr int warps = NMAT * BN >= 64 ? 8 : 4;
   static constexpr int threads = 64 + 32 * warps;  // TMA warp, MMA warp
   static constexpr int tokens = BN * 4 / warps;    // of one epilogue thread
   static constexpr int stage_bytes = NMAT * FBS_WTILE + BN * 128;
@@ -199,11 +199,11 @@ __global__ void __launch_bounds__(FbsShape<NMAT, BN>::threads)
     const uint32_t base = tmem + (static_cast<uint32_t>(32 * q) << 16) + t0;
     constexpr int SL = (TN + 31) / 32;  // tokens a lane loads scales for
     float *comb = s_comb + ew * 2 * NMAT * TN;
-    float acc[NMAT][TN];
+    uint64_t acc[NMAT][TN / 2];  // pairs of tokens
 #pragma unroll
     for (int m = 0; m < NMAT; ++m)
 #pragma unroll
-      for (int n = 0; n < TN; ++n) acc[m][n] = 0.f;
+      for (int n = 0; n < TN / 2; ++n) acc[m][n] = 0ull;
     float psx[FBS_PRE][SL], psw[FBS_PRE][NMAT];
     pdl_wait();  // s_x comes from the previous kernel
     auto fetch = [&](int i, float (&sx)[SL], float (&sw)[NMAT]) {
@@ -253,11 +253,10 @@ __global__ void __launch_bounds__(FbsShape<NMAT, BN>::threads)
               for (int m = 0; m < NMAT; ++m)
 #pragma unroll
                 for (int e = 0; e < CH; e += 4) {
-                  const float4 w = *reinterpret_cast<const float4 *>(cb + m * TN + c + e);
-                  acc[m][c + e + 0] = fmaf(d[m][e + 0], w.x, acc[m][c + e + 0]);
-                  acc[m][c + e + 1] = fmaf(d[m][e + 1], w.y, acc[m][c + e + 1]);
-                  acc[m][c + e + 2] = fmaf(d[m][e + 2], w.z, acc[m][c + e + 2]);
-                  acc[m][c + e + 3] = fmaf(d[m][e + 3], w.w, acc[m][c + e + 3]);
+                  const ulonglong2 w = *reinterpret_cast<const ulonglong2 *>(cb + m * TN + c + e);
+                  uint64_t *s = &acc[m][(c + e) / 2];
+                  s[0] = fma_f32x2(pack_f32x2(d[m][e], d[m][e + 1]), w.x, s[0]);
+                  s[1] = fma_f32x2(pack_f32x2(d[m][e + 2], d[m][e + 3]), w.y, s[1]);
                 }
             }
             tc_fence_before();
@@ -274,7 +273,12 @@ __global__ void __launch_bounds__(FbsShape<NMAT, BN>::threads)
 #pragma unroll
       for (int m = 0; m < NMAT; ++m)
 #pragma unroll
-        for (int n = 0; n < TN; ++n) part[(m * BN + t0 + n) * 128 + row] = acc[m][n];
+        for (int n = 0; n < TN / 2; ++n) {
+          float lo, hi;
+          unpack_f32x2(acc[m][n], lo, hi);
+          part[(m * BN + t0 + 2 * n) * 128 + row] = lo;
+          part[(m * BN + t0 + 2 * n + 1) * 128 + row] = hi;
+        }
   }
 
   // TMEM is released and the copies in flight are waited for before the
