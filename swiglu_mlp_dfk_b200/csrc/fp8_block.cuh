@@ -90,9 +90,7 @@ __device__ __forceinline__ float fb_silu_mul(float a, float u) {
 // Bounded mbarrier wait, as mbar_wait_bounded (same limits, same abort flag and
 // error word), for waits that usually end within a microsecond and follow one
 // another: the clock, the limit (a global load) and the abort flag are only
-// looked at every 256 tries.  Reading the limit after the first failed try
-// made each hand-over of an accumulator cost a trip to L2: 1.3 us per group of
-// 128 instead of 0.3 (4096 x 4096 x 14336).
+// looked at every 256 tries.
 __device__ __forceinline__ bool fb_wait(uint64_t *bar, uint32_t parity, volatile int *abort_flag,
                                         unsigned *err) {
   unsigned long long t0 = 0, limit = 0;
@@ -121,7 +119,9 @@ __device__ __forceinline__ uint32_t cluster_rank() {
   return r;
 }
 
+// Every thread of every CTA of the cluster; the warps converge first.
 __device__ __forceinline__ void cluster_sync_all() {
+  __syncwarp();
   asm volatile("barrier.cluster.arrive.release.aligned;\n\t"
                "barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
