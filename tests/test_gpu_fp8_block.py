@@ -70,7 +70,9 @@ def activations(g, M, K):
 
 
 def weights(g, N, K, std=0.05):
-    return I.to_fp8_blocks(std * torch.randn(N, K, generator=g, device="cuda"))
+    w = I.to_fp8_blocks(std * torch.randn(N, K, generator=g, device="cuda"))
+    torch.cuda.synchronize()      # weights are read before the previous kernel has finished
+    return w
 
 
 def sum_error(G):
@@ -204,6 +206,21 @@ def test_add_rmsnorm_in_place_and_zero_rows():
         assert torch.equal(q.view(torch.uint8), q0.view(torch.uint8)) and torch.equal(s, s0)
 
 
+@pytest.mark.parametrize("M", [5, 1100])
+def test_add_rmsnorm_in_place_of_every_size(M):
+    g = gen(M)
+    x, res = rand_bf16(g, M, 1040), rand_bf16(g, M, 1040)
+    x[0, :8] = 2.0 ** -133                       # subnormal bf16 sums are kept
+    res[0, :8] = 2.0 ** -133
+    gamma = rand_bf16(g, 1040)
+    q0, s0, r0 = dfk.dfk_add_rmsnorm_fp8_block(x, res, gamma, 1e-5)
+    assert torch.equal(r0, (x.float() + res.float()).bfloat16())
+    assert (r0[0, :8] == 2.0 ** -132).all()
+    q, s, r = dfk.dfk_add_rmsnorm_fp8_block(x, res, gamma, 1e-5, residual_out=res)
+    assert r is res and torch.equal(r, r0) and torch.equal(s, s0)
+    assert torch.equal(q.view(torch.uint8), q0.view(torch.uint8))
+
+
 def test_add_rmsnorm_all_zero_row_with_zero_eps_is_nan_as_the_formula():
     x = torch.zeros(2, 256, device="cuda", dtype=torch.bfloat16)
     x[1] = 1
@@ -245,6 +262,43 @@ def test_gate_up(M, D, F, fp8_out):
         check_quantised(*out, ref, err)
     else:
         check_rounded(out, ref, err, 2.0 ** -8)
+
+
+# Sizes of the tensor-bound kernel's forms: pairs of CTAs, single CTAs (fewer rounds of tiles),
+# clusters that share a tile's groups; odd columns, part tiles, shorter last groups.
+@pytest.mark.parametrize("M,K,N", [(1100, 400, 5001), (2300, 272, 4112), (400, 272, 9008),
+                                   (330, 144, 12296), (192, 14336, 4001), (150, 4112, 2048)])
+@pytest.mark.parametrize("op", ["gemm", "fp8", "bf16"])
+def test_forms_for_many_tokens(M, K, N, op):
+    g = gen(M + K)
+    q_x, s_x = activations(g, M, K)
+    if op == "gemm":
+        w = weights(g, N, K)
+        check_rounded(dfk.dfk_gemm_fp8_block(q_x, s_x, *w), *product(q_x, s_x, *w), 2.0 ** -8)
+        return
+    if op == "fp8":
+        N = -(-N // 16) * 16
+    N = min(N, 6000) if K > 4000 else N
+    wg, wu = weights(g, N, K), weights(g, N, K)
+    out = dfk.dfk_swiglu_gate_up_fp8_block(q_x, s_x, *wg, *wu, fp8_out=op == "fp8")
+    ref, err = silu_mul(*product(q_x, s_x, *wg), *product(q_x, s_x, *wu))
+    if op == "fp8":
+        check_quantised(*out, ref, err)
+    else:
+        check_rounded(out, ref, err, 2.0 ** -8)
+
+
+def test_codes_as_bytes():
+    g = gen(8)
+    q_x, s_x = activations(g, 70, 256)
+    q_w, s_w = weights(g, 128, 256)
+    u8 = torch.uint8
+    y = dfk.dfk_gemm_fp8_block(q_x, s_x, q_w, s_w)
+    assert torch.equal(y, dfk.dfk_gemm_fp8_block(q_x.view(u8), s_x, q_w.view(u8), s_w))
+    q = torch.empty(70, 128, dtype=u8, device="cuda")
+    want, s = dfk.dfk_quant_fp8_block(y)
+    got, s2 = dfk.dfk_quant_fp8_block(y, q=q)
+    assert got is q and torch.equal(q, want.view(u8)) and torch.equal(s, s2)
 
 
 def test_silu_far_from_zero():
@@ -458,6 +512,53 @@ def test_large_offsets():
         a, b = q_x[lo:lo + 64].contiguous(), s_x[:, lo:lo + 64].contiguous()
         ref, err = product(a, b, q_w, s_w)
         check_rounded(y[lo:lo + 64], ref, err, 2.0 ** -8)
+
+
+def test_a_given_stream_in_a_capture_and_as_a_handle():
+    g = gen(4)
+    layer, x, res = Layer(g, 256, 512), rand_bf16(g, 9, 256), rand_bf16(g, 9, 256)
+    want = layer(x, res)
+    torch.cuda.synchronize()
+    assert same(layer(x, res, stream=0), want)                    # the legacy default stream
+    st = torch.cuda.Stream()
+    got = layer(x, res, stream=st.cuda_stream)
+    st.synchronize()
+    assert same(got, want)
+    gr = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(gr, stream=st):
+        out = layer(x, res, stream=st)
+    for t in out:
+        t.view(torch.uint8).fill_(3)
+    torch.cuda.synchronize()
+    gr.replay()
+    torch.cuda.synchronize()
+    assert same(out, want)
+
+
+FIRST = r'''
+import os, sys
+sys.path.insert(0, os.environ["DFK_ROOT"])
+sys.path.insert(0, os.path.join(os.environ["DFK_ROOT"], "tests"))
+import torch
+import swiglu_mlp_dfk_b200 as dfk
+import test_gpu_fp8_block as t
+g = t.gen(1)
+layer, x, res = t.Layer(g, 512, 1024), t.rand_bf16(g, 300, 512), t.rand_bf16(g, 300, 512)
+torch.cuda.synchronize()
+gr = torch.cuda.CUDAGraph()
+with torch.cuda.graph(gr):
+    out = layer(x, res)
+gr.replay()
+torch.cuda.synchronize()
+assert t.same(out, layer(x, res))
+print("first call in a capture ok")
+'''
+
+
+def test_the_first_call_may_be_captured():
+    r = subprocess.run([sys.executable, "-c", FIRST], env=dict(os.environ, DFK_ROOT=ROOT),
+                       capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "capture ok" in r.stdout, r.stdout + r.stderr
 
 
 def test_no_tokens():
