@@ -362,7 +362,8 @@ def dfk_rmsnorm_qkv_proj(x, gamma, eps, w_qkv, n_q, n_k, n_v, q=None, k=None, v=
 _E4M3 = torch.float8_e4m3fn
 _FP8_CODES = (_E4M3, torch.uint8)
 _BF16_ONLY = (_BF16,)
-_F32_ONLY = (torch.float32,)
+_F32 = torch.float32
+_F32_ONLY = (_F32,)
 _Tensor = torch.Tensor
 _get_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
@@ -377,7 +378,6 @@ def _fb_refuse(name, t, dtypes, shape, dev):
     raise DfkError(DFK_ERR_INVALID_ARG, "%s %s" % (name, why))
 
 
-# Up to seven of these a call: a few attribute reads each (0.4 us).
 def _fb_check(name, t, dtypes, shape, dev):
     if not (isinstance(t, _Tensor) and t.dtype in dtypes and t.shape == shape
             and t.get_device() == dev and t.is_contiguous()):
@@ -390,6 +390,49 @@ def _fb_rows(name, t):
         raise DfkError(DFK_ERR_INVALID_ARG, "%s must be a 2-D CUDA tensor" % name)
     shape = t.shape
     return shape[0], shape[1], t.get_device()
+
+
+# A call on a small tensor is bound by its Python (a launch takes 3 us, the kernels 1-2): the
+# entry points test their operands in one expression of attribute reads (0.1 us each) and go
+# through the checks above, which name the fault, only where it fails.
+
+def _fb_activations(name, t):
+    """(M, K, device index) of a bf16 activation tensor."""
+    try:
+        M, K = t.shape
+        dev = t.get_device()
+        if t.dtype is _BF16 and dev >= 0 and t.is_contiguous():
+            return M, K, dev
+    except (AttributeError, TypeError, ValueError):
+        pass
+    M, K, dev = _fb_rows(name, t)
+    _fb_refuse(name, t, _BF16_ONLY, (M, K), dev)
+
+
+def _fb_operands(q_x, s_x, q_w, s_w, name):
+    """(M, K, N, groups of K, device index) of a product's operands."""
+    try:
+        M, K = q_x.shape
+        N, K_w = q_w.shape
+        G = (K + 127) >> 7
+        dev = q_x.get_device()
+        if (q_x.dtype in _FP8_CODES and q_w.dtype in _FP8_CODES and s_x.dtype is _F32
+                and s_w.dtype is _F32 and K_w == K and s_x.shape == (G, M)
+                and s_w.shape == ((N + 127) >> 7, G)
+                and 0 <= dev == s_x.get_device() == q_w.get_device() == s_w.get_device()
+                and q_x.is_contiguous() and s_x.is_contiguous() and q_w.is_contiguous()
+                and s_w.is_contiguous()):
+            return M, K, N, G, dev
+    except (AttributeError, TypeError, ValueError):
+        pass
+    M, K, dev = _fb_rows("q_x", q_x)
+    N = _fb_rows(name, q_w)[0]
+    G = (K + 127) >> 7
+    _fb_check("q_x", q_x, _FP8_CODES, (M, K), dev)
+    _fb_check("s_x", s_x, _F32_ONLY, (G, M), dev)
+    _fb_check(name, q_w, _FP8_CODES, (N, K), dev)
+    _fb_check("s" + name[1:], s_w, _F32_ONLY, ((N + 127) >> 7, G), dev)
+    return M, K, N, G, dev
 
 
 def _fb_call(dev, stream, fn, *args):
@@ -413,16 +456,16 @@ def _fb_keep(t, stream):
                         else torch.cuda.ExternalStream(int(stream), device=t.device))
 
 
-def _fb_codes_out(q, s, M, K, dev, stream, like):
-    G = (K + 127) // 128
+def _fb_codes_out(q, s, M, K, dev, stream, device):
+    G = (K + 127) >> 7
     if q is None:
-        q = torch.empty(M, K, dtype=_E4M3, device=like.device)  # separate sizes: 1 us less
+        q = torch.empty(M, K, dtype=_E4M3, device=device)  # separate sizes: 1 us less
         if stream is not None:
             _fb_keep(q, stream)
     else:
         _fb_check("q", q, _FP8_CODES, (M, K), dev)
     if s is None:
-        s = torch.empty(G, M, dtype=torch.float32, device=like.device)
+        s = torch.empty(G, M, dtype=_F32, device=device)
         if stream is not None:
             _fb_keep(s, stream)
     else:
@@ -433,11 +476,10 @@ def _fb_codes_out(q, s, M, K, dev, stream, like):
 def dfk_quant_fp8_block(x, q=None, s=None, stream=None):
     """Block-scaled FP8 of x [M, K] bf16: returns (q [M, K] float8_e4m3fn, s [ceil(K/128), M]
     fp32), s = max(max|x| / 448, 2^-126) per token and group of 128, q = E4M3(x / s)."""
-    M, K, dev = _fb_rows("x", x)
-    _fb_check("x", x, _BF16_ONLY, (M, K), dev)
-    q, s = _fb_codes_out(q, s, M, K, dev, stream, x)
-    _fb_call(dev, stream, lib().dfk_quant_fp8_block, x.data_ptr(), q.data_ptr(), s.data_ptr(), M,
-             K)
+    M, K, dev = _fb_activations("x", x)
+    q, s = _fb_codes_out(q, s, M, K, dev, stream, x.device)
+    _fb_call(dev, stream, (_lib or lib()).dfk_quant_fp8_block, x.data_ptr(), q.data_ptr(),
+             s.data_ptr(), M, K)
     return q, s
 
 
@@ -446,32 +488,24 @@ def dfk_add_rmsnorm_fp8_block(x, residual, gamma, eps, residual_out=None, q=None
     """r = bf16(x + residual) (r = x for residual None), then the block-scaled FP8 of
     RMSNorm(r; gamma, eps): returns (q, s, r), r None without a residual.  residual_out may be
     `residual` or `x` itself: the sum is then kept in place."""
-    M, D, dev = _fb_rows("x", x)
-    _fb_check("x", x, _BF16_ONLY, (M, D), dev)
+    M, D, dev = _fb_activations("x", x)
     _fb_check("gamma", gamma, _BF16_ONLY, (D,), dev)
+    p_res = p_out = None
     if residual is not None:
         _fb_check("residual", residual, _BF16_ONLY, (M, D), dev)
+        p_res = residual.data_ptr()
         if residual_out is None:
             residual_out = torch.empty_like(residual)
             if stream is not None:
                 _fb_keep(residual_out, stream)
-    if residual_out is not None:
+            p_out = residual_out.data_ptr()
+    if residual_out is not None and p_out is None:
         _fb_check("residual_out", residual_out, _BF16_ONLY, (M, D), dev)
-    q, s = _fb_codes_out(q, s, M, D, dev, stream, x)
-    _fb_call(dev, stream, lib().dfk_add_rmsnorm_fp8_block, x.data_ptr(), _ptr(residual),
-             gamma.data_ptr(), float(eps), _ptr(residual_out), q.data_ptr(), s.data_ptr(), M, D)
+        p_out = residual_out.data_ptr()
+    q, s = _fb_codes_out(q, s, M, D, dev, stream, x.device)
+    _fb_call(dev, stream, (_lib or lib()).dfk_add_rmsnorm_fp8_block, x.data_ptr(), p_res,
+             gamma.data_ptr(), float(eps), p_out, q.data_ptr(), s.data_ptr(), M, D)
     return q, s, residual_out
-
-
-def _fb_operands(q_x, s_x, q_w, s_w, name):
-    M, K, dev = _fb_rows("q_x", q_x)
-    N = _fb_rows(name, q_w)[0]
-    G = (K + 127) // 128
-    _fb_check("q_x", q_x, _FP8_CODES, (M, K), dev)
-    _fb_check("s_x", s_x, _F32_ONLY, (G, M), dev)
-    _fb_check(name, q_w, _FP8_CODES, (N, K), dev)
-    _fb_check("s" + name[1:], s_w, _F32_ONLY, ((N + 127) // 128, G), dev)
-    return M, K, N, G, dev
 
 
 def dfk_gemm_fp8_block(q_x, s_x, q_w, s_w, y=None, stream=None):
@@ -485,7 +519,7 @@ def dfk_gemm_fp8_block(q_x, s_x, q_w, s_w, y=None, stream=None):
             _fb_keep(y, stream)
     else:
         _fb_check("y", y, _BF16_ONLY, (M, N), dev)
-    _fb_call(dev, stream, lib().dfk_gemm_fp8_block, q_x.data_ptr(), s_x.data_ptr(),
+    _fb_call(dev, stream, (_lib or lib()).dfk_gemm_fp8_block, q_x.data_ptr(), s_x.data_ptr(),
              q_w.data_ptr(), s_w.data_ptr(), y.data_ptr(), M, K, N)
     return y
 
@@ -497,12 +531,13 @@ def dfk_swiglu_gate_up_fp8_block(q_x, s_x, q_gate, s_gate, q_up, s_up, fp8_out=T
     fp32 values; otherwise returns h [M, d_ff] bf16."""
     M, D, F, G, dev = _fb_operands(q_x, s_x, q_gate, s_gate, "q_gate")
     _fb_check("q_up", q_up, _FP8_CODES, (F, D), dev)
-    _fb_check("s_up", s_up, _F32_ONLY, ((F + 127) // 128, G), dev)
+    _fb_check("s_up", s_up, _F32_ONLY, ((F + 127) >> 7, G), dev)
+    ph = pq = ps = None
     if fp8_out:
         if h is not None:
             raise DfkError(DFK_ERR_INVALID_ARG, "h is the bf16 output: fp8_out=False")
-        q_h, s_h = _fb_codes_out(q_h, s_h, M, F, dev, stream, s_x)
-        ph, pq, ps = None, q_h.data_ptr(), s_h.data_ptr()
+        q_h, s_h = _fb_codes_out(q_h, s_h, M, F, dev, stream, s_x.device)
+        pq, ps = q_h.data_ptr(), s_h.data_ptr()
     else:
         if q_h is not None or s_h is not None:
             raise DfkError(DFK_ERR_INVALID_ARG, "q_h and s_h are the FP8 output: fp8_out=True")
@@ -512,10 +547,10 @@ def dfk_swiglu_gate_up_fp8_block(q_x, s_x, q_gate, s_gate, q_up, s_up, fp8_out=T
                 _fb_keep(h, stream)
         else:
             _fb_check("h", h, _BF16_ONLY, (M, F), dev)
-        ph, pq, ps = h.data_ptr(), None, None
-    _fb_call(dev, stream, lib().dfk_swiglu_gate_up_fp8_block, q_x.data_ptr(), s_x.data_ptr(),
-             q_gate.data_ptr(), s_gate.data_ptr(), q_up.data_ptr(), s_up.data_ptr(), ph, pq, ps,
-             M, D, F)
+        ph = h.data_ptr()
+    _fb_call(dev, stream, (_lib or lib()).dfk_swiglu_gate_up_fp8_block, q_x.data_ptr(),
+             s_x.data_ptr(), q_gate.data_ptr(), s_gate.data_ptr(), q_up.data_ptr(),
+             s_up.data_ptr(), ph, pq, ps, M, D, F)
     return (q_h, s_h) if fp8_out else h
 
 
