@@ -126,6 +126,20 @@ __device__ __forceinline__ void cluster_sync_all() {
                "barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
+// As cluster_sync_all, ordering nothing: for CTAs that only wait until the others
+// have read their shared memory (every value read has been used by then).  The
+// release of the ordered form waits for the thread's global stores, 0.8 us at
+// the end of a call.
+__device__ __forceinline__ void cluster_sync_relaxed() {
+  __syncwarp();
+  asm volatile("barrier.cluster.arrive.relaxed.aligned;\n\t"
+               "barrier.cluster.wait.aligned;" ::: "memory");
+}
+
+__device__ __forceinline__ void tensormap_prefetch(const CUtensorMap *m) {
+  asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(m)) : "memory");
+}
+
 // Address of the same shared-memory location in CTA `rank` of the cluster.
 __device__ __forceinline__ uint32_t cluster_map(uint32_t saddr, uint32_t rank) {
   uint32_t r;
@@ -156,17 +170,17 @@ __device__ __forceinline__ void fb_sum_shares(uint32_t at, uint32_t vstep, int k
     for (int r = 0; r < 4; ++r)
 #pragma unroll
       for (int v = 0; v < NV; ++v)
-        o[r][v] = ld_cluster_f4(cluster_map(at + v * vstep, min(r0 + r, ks - 1)));
+        o[r][v] = r0 + r < ks ? ld_cluster_f4(cluster_map(at + v * vstep, r0 + r))
+                              : make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
     for (int r = 0; r < 4; ++r)
 #pragma unroll
-      for (int v = 0; v < NV; ++v)
-        if (r0 + r < ks) {
-          sum[v].x += o[r][v].x;
-          sum[v].y += o[r][v].y;
-          sum[v].z += o[r][v].z;
-          sum[v].w += o[r][v].w;
-        }
+      for (int v = 0; v < NV; ++v) {
+        sum[v].x += o[r][v].x;
+        sum[v].y += o[r][v].y;
+        sum[v].z += o[r][v].z;
+        sum[v].w += o[r][v].w;
+      }
   }
 }
 
@@ -192,8 +206,8 @@ struct FbParams {
   int stages;
 };
 
-// Output of one token's 128 weight rows (block `blk`) by a whole warp, four
-// rows a lane: bf16, or codes and the group's scale.
+// bf16 output of one token's 128 weight rows (block `blk`) by a whole warp, four
+// rows a lane.
 template <int NMAT>
 __device__ __forceinline__ void fb_emit4(const FbParams &p, int m, int blk, int lane,
                                          const float4 &a, const float4 &up) {
@@ -201,27 +215,76 @@ __device__ __forceinline__ void fb_emit4(const FbParams &p, int m, int blk, int 
   float h[4] = {a.x, a.y, a.z, a.w};
   const float u[4] = {up.x, up.y, up.z, up.w};
 #pragma unroll
-  for (int e = 0; e < 4; ++e) {
+  for (int e = 0; e < 4; ++e)
     if (NMAT == 2) h[e] = fb_silu_mul(h[e], u[e]);
-    if (j + e >= p.N) h[e] = 0.f;
-  }
-  const size_t at = static_cast<size_t>(m) * p.N + j;
-  if (NMAT == 2 && p.y == nullptr) {
-    float mx = max_nan(max_nan(fabsf(h[0]), fabsf(h[1])), max_nan(fabsf(h[2]), fabsf(h[3])));
-#pragma unroll
-    for (int d = 16; d >= 1; d >>= 1) mx = max_nan(mx, __shfl_xor_sync(0xffffffffu, mx, d));
-    const FbScale f = fb_scale(mx);
-    if (j < p.N && DFK_IN_BOUNDS(j + 4 <= p.N && m < p.M, 28, p.err))
-      *reinterpret_cast<uint32_t *>(p.qh + at) = fb_codes4(h[0], h[1], h[2], h[3], f);
-    if (lane == 0) p.sh[static_cast<size_t>(blk) * p.M + m] = f.s;
-  } else if ((p.N & 3) == 0) {
+  uint16_t *at = p.y + static_cast<size_t>(m) * p.N + j;
+  if ((p.N & 3) == 0) {
     if (j < p.N && DFK_IN_BOUNDS(j + 4 <= p.N && m < p.M, 29, p.err))
-      *reinterpret_cast<uint2 *>(p.y + at) = make_uint2(pack_bf16x2(h[0], h[1]),
-                                                        pack_bf16x2(h[2], h[3]));
+      *reinterpret_cast<uint2 *>(at) =
+          make_uint2(pack_bf16x2(h[0], h[1]), pack_bf16x2(h[2], h[3]));
   } else {
 #pragma unroll
     for (int e = 0; e < 4; ++e)
-      if (j + e < p.N && DFK_IN_BOUNDS(m < p.M, 30, p.err)) p.y[at + e] = f32_to_bf16_bits(h[e]);
+      if (j + e < p.N && DFK_IN_BOUNDS(m < p.M, 30, p.err)) at[e] = f32_to_bf16_bits(h[e]);
+  }
+}
+
+// Quantised output of a gated product: nt tokens (the first is token m0), weight
+// rows of block `blk` (one group), summed over the cluster's CTAs in rank order.
+// at: shared-memory address of token 0's 128 gate sums, `tstep` bytes from token to
+// token, `mstep` from a token's gate sums to its up sums.  Eight lanes take a
+// token, sixteen rows each; this warp is the w-th of nw in CTA `rank`.  (A token a
+// turn and warp: 64 tokens took 3 us, each a chain of loads, SiLU, five shuffles,
+// two reciprocals.)
+__device__ __forceinline__ void fb_emit_codes(const FbParams &p, uint32_t at, uint32_t tstep,
+                                              uint32_t mstep, int nt, int m0, int blk, int w,
+                                              int nw, int rank, int ks, int lane) {
+  const int l = lane & 7;
+  for (int quad = rank * nw + w; 4 * quad < nt; quad += nw * ks) {
+    const int n = 4 * quad + (lane >> 3);
+    const uint32_t mine = at + static_cast<uint32_t>(min(n, nt - 1)) * tstep + 16 * l;
+    float h[16], u[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) h[i] = u[i] = 0.f;
+    for (int r = 0; r < ks; ++r) {
+      const uint32_t src = cluster_map(mine, ks == 1 ? rank : r);
+      float4 g[4], v[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        g[i] = ld_cluster_f4(src + 128 * i);
+        v[i] = ld_cluster_f4(src + 128 * i + mstep);
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        h[4 * i] += g[i].x;
+        h[4 * i + 1] += g[i].y;
+        h[4 * i + 2] += g[i].z;
+        h[4 * i + 3] += g[i].w;
+        u[4 * i] += v[i].x;
+        u[4 * i + 1] += v[i].y;
+        u[4 * i + 2] += v[i].z;
+        u[4 * i + 3] += v[i].w;
+      }
+    }
+    const int j = blk * 128 + 4 * l;  // and 32 further on for each i
+    float mx = 0.f;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      h[i] = fb_silu_mul(h[i], u[i]);
+      if (j + 32 * (i >> 2) < p.N) mx = max_nan(mx, fabsf(h[i]));  // N % 16 == 0
+    }
+#pragma unroll
+    for (int d = 4; d >= 1; d >>= 1) mx = max_nan(mx, __shfl_xor_sync(0xffffffffu, mx, d));
+    const FbScale f = fb_scale(mx);
+    if (n < nt) {
+      uint8_t *q = p.qh + static_cast<size_t>(m0 + n) * p.N + j;
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (j + 32 * i < p.N && DFK_IN_BOUNDS(j + 32 * i + 4 <= p.N && m0 + n < p.M, 28, p.err))
+          *reinterpret_cast<uint32_t *>(q + 32 * i) =
+              fb_codes4(h[4 * i], h[4 * i + 1], h[4 * i + 2], h[4 * i + 3], f);
+      if (l == 0) p.sh[static_cast<size_t>(blk) * p.M + m0 + n] = f.s;
+    }
   }
 }
 

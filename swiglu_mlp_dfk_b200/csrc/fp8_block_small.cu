@@ -95,7 +95,22 @@ __global__ void __launch_bounds__(FbsShape<NMAT, BN>::threads)
   const int kb1 = static_cast<int>(static_cast<long long>(rank + 1) * p.G / ks);
   const int nkb = kb1 - kb0;
 
+  // Thread 0 sets the barriers up and at once sends for the weights of the first
+  // stages (before the dependency on the previous kernel; the activation codes
+  // follow after it).
+  const uint64_t pol_w = gridDim.y > 1 ? l2_policy_evict_normal() : l2_policy_evict_first();
+  const int S0 = min(S, nkb);
+  auto load_w = [&](int i, int st) {
+    uint8_t *sb = smem + st * Sh::stage_bytes;
+    mbar_arrive_expect_tx(&fullb[st], Sh::stage_bytes);
+#pragma unroll
+    for (int m = 0; m < NMAT; ++m)
+      tma_load_2d(sb + m * FBS_WTILE, &maps.w[m], &fullb[st], (kb0 + i) * 128, j0, pol_w);
+  };
   if (tid == 0) {
+#pragma unroll
+    for (int m = 0; m < NMAT; ++m) tensormap_prefetch(&maps.w[m]);
+    tensormap_prefetch(&maps.x);
     for (int s = 0; s < S; ++s) {
       mbar_init(&fullb[s], 1);
       mbar_init(&empty[s], 1);
@@ -108,6 +123,8 @@ __global__ void __launch_bounds__(FbsShape<NMAT, BN>::threads)
     *s_abort = 0;
     *s_issued = 0;
     fence_mbar_init();
+    fence_proxy_async_smem();
+    for (int i = 0; i < S0; ++i) load_w(i, i);
   }
   if (warp == 1) {
     tmem_alloc(s_tmem, Sh::tmem_cols);
@@ -120,24 +137,13 @@ __global__ void __launch_bounds__(FbsShape<NMAT, BN>::threads)
   pdl_launch_dependents();
 
   if (warp == 0) {
-    // ---- TMA: weights of the first S stages before the dependency, the
-    // activation codes after it
+    // ---- TMA
     if (lane == 0) {
-      const uint64_t pol_w = gridDim.y > 1 ? l2_policy_evict_normal() : l2_policy_evict_first();
       const uint64_t pol_x = l2_policy_evict_normal();
-      const int S0 = min(S, nkb);
-      auto load_w = [&](int i, int st) {
-        uint8_t *sb = smem + st * Sh::stage_bytes;
-        mbar_arrive_expect_tx(&fullb[st], Sh::stage_bytes);
-#pragma unroll
-        for (int m = 0; m < NMAT; ++m)
-          tma_load_2d(sb + m * FBS_WTILE, &maps.w[m], &fullb[st], (kb0 + i) * 128, j0, pol_w);
-      };
       auto load_x = [&](int i, int st) {
         tma_load_2d(smem + st * Sh::stage_bytes + NMAT * FBS_WTILE, &maps.x, &fullb[st],
                     (kb0 + i) * 128, n0, pol_x);
       };
-      for (int i = 0; i < S0; ++i) load_w(i, i);
       pdl_wait();
       for (int i = 0; i < S0; ++i) load_x(i, i);
       int issued = S0, st = 0;
@@ -305,7 +311,9 @@ __global__ void __launch_bounds__(FbsShape<NMAT, BN>::threads)
     // one token per warp and turn, spread over the cluster's CTAs; lane l
     // takes rows 4 l .. 4 l + 3
     const int nt = min(BN, p.M - n0);
-    if (ks == 1) {
+    if (NMAT == 2 && p.y == nullptr) {
+      fb_emit_codes(p, sbase, 512, BN * 512, nt, n0, blk, warp - 2, Sh::warps, rank, ks, lane);
+    } else if (ks == 1) {
       // four tokens' sums in registers at a time: one after the other, a round
       // trip each, cost up to 2 us
       for (int n = warp - 2; n < nt; n += 4 * Sh::warps) {
@@ -331,7 +339,7 @@ __global__ void __launch_bounds__(FbsShape<NMAT, BN>::threads)
     }
   }
   __syncwarp();
-  if (ks > 1) cluster_sync_all();  // no CTA leaves while its sums are being read
+  if (ks > 1) cluster_sync_relaxed();  // no CTA leaves while its sums are being read
 }
 
 template <int NMAT, int BN>
