@@ -229,6 +229,27 @@ __device__ __forceinline__ void fb_emit4(const FbParams &p, int m, int blk, int 
   }
 }
 
+// Quantised output of a gated product, one token by a whole warp.
+__device__ __forceinline__ void fb_emit4_codes(const FbParams &p, int m, int blk, int lane,
+                                               const float4 &a, const float4 &up) {
+  const int j = blk * 128 + 4 * lane;
+  float h[4] = {a.x, a.y, a.z, a.w};
+  const float u[4] = {up.x, up.y, up.z, up.w};
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    h[e] = fb_silu_mul(h[e], u[e]);
+    if (j + e >= p.N) h[e] = 0.f;
+  }
+  float mx = max_nan(max_nan(fabsf(h[0]), fabsf(h[1])), max_nan(fabsf(h[2]), fabsf(h[3])));
+#pragma unroll
+  for (int d = 16; d >= 1; d >>= 1) mx = max_nan(mx, __shfl_xor_sync(0xffffffffu, mx, d));
+  const FbScale f = fb_scale(mx);
+  if (j < p.N && DFK_IN_BOUNDS(j + 4 <= p.N && m < p.M, 35, p.err))
+    *reinterpret_cast<uint32_t *>(p.qh + static_cast<size_t>(m) * p.N + j) =
+        fb_codes4(h[0], h[1], h[2], h[3], f);
+  if (lane == 0) p.sh[static_cast<size_t>(blk) * p.M + m] = f.s;
+}
+
 // Quantised output of a gated product: nt tokens (the first is token m0), weight
 // rows of block `blk` (one group), summed over the cluster's CTAs in rank order.
 // at: shared-memory address of token 0's 128 gate sums, `tstep` bytes from token to

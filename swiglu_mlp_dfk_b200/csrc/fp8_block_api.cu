@@ -62,7 +62,7 @@ static SmallPlan plan_small(const FbCall &c, int G, int sms) {
   const int limit = s.pack ? 2 * sms : sms;
   s.ks = 1;
   while (s.ks < 8 && work * s.ks * 2 <= limit && s.ks * 8 <= G) s.ks *= 2;
-  s.us = 5.0 + 0.57 * ceil_div(G, s.ks) * ceil_div(work * s.ks, limit);
+  s.us = 4.5 + 0.53 * ceil_div(G, s.ks) * ceil_div(work * s.ks, limit);
   return s;
 }
 
@@ -91,8 +91,8 @@ static LargePlan plan_large(const FbCall &c, int G, int sms) {
 // `us` above: what a call takes, fitted to 30 shapes of 48 to 4096 tokens on a
 // B200: a fixed part (launch, first loads, output; 4 us more where a cluster adds
 // its shares) and a part per group and round of tiles.  Both sides at 192 tokens:
-// N = 6144, K = 4096 15.5 us streaming, 17.9 by pairs; N = 4096, K = 14336 36 us
-// streaming, 24 by clusters of 4, 47 by pairs; N = 16384, K = 4096 41, 21.5, 20.
+// N = 6144, K = 4096 14.0 us streaming, 17.8 by pairs; N = 4096, K = 14336 33.6 us
+// streaming, 23.1 by clusters of 4, 46.5 by pairs; N = 16384, K = 4096 41, 21.5, 20.
 static int launch_small(const FbCall &c, const SmallPlan &s, int G, unsigned *err,
                         cudaStream_t st) {
   if (s.tiles > 65535) return api_fail(DFK_ERR_UNSUPPORTED_SHAPE, "M=%d is too large", c.M);

@@ -616,20 +616,16 @@ __global__ void __launch_bounds__(FBL_THREADS, 1)
       int tm, tn;
       tiles.at(unit, tm, tn);
       const int nt = min(128, p.M - tm * 128);
-      if (GATE && p.y == nullptr) {
-        fb_emit_codes(p, sbase, FBL_PART_ROW, 512, nt, tm * 128, tn, warp - 4, 8, kr, ks, lane);
-      } else {
-        for (int n = kr * 8 + (warp - 4); n < nt; n += 8 * ks) {
-          float4 a[2];
-          fb_sum_shares<2>(sbase + static_cast<uint32_t>(n * FBL_PART_ROW + 16 * lane), 512, ks,
-                           a);
-          const int m = tm * 128 + n;
-          if constexpr (GATE) {
-            fb_emit4<2>(p, m, tn, lane, a[0], a[1]);
-          } else {
-            fb_emit4<1>(p, m, 2 * tn, lane, a[0], a[0]);
-            fb_emit4<1>(p, m, 2 * tn + 1, lane, a[1], a[1]);
-          }
+      for (int n = kr * 8 + (warp - 4); n < nt; n += 8 * ks) {
+        float4 a[2];
+        fb_sum_shares<2>(sbase + static_cast<uint32_t>(n * FBL_PART_ROW + 16 * lane), 512, ks, a);
+        const int m = tm * 128 + n;
+        if constexpr (GATE) {
+          if (p.y == nullptr) fb_emit4_codes(p, m, tn, lane, a[0], a[1]);
+          else fb_emit4<2>(p, m, tn, lane, a[0], a[1]);
+        } else {
+          fb_emit4<1>(p, m, 2 * tn, lane, a[0], a[0]);
+          fb_emit4<1>(p, m, 2 * tn + 1, lane, a[1], a[1]);
         }
       }
     }
