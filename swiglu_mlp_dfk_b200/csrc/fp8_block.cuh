@@ -203,7 +203,8 @@ struct FbParams {
   float *sh;           // [ceil(N / 128)][M]
   unsigned *err;
   int M, N, G;
-  int stages;
+  int stages;          // streaming kernel: ring stages
+  int band;            // tensor-bound kernel: token tiles of a band
 };
 
 // bf16 output of one token's 128 weight rows (block `blk`) by a whole warp, four

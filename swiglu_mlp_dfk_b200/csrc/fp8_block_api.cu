@@ -109,7 +109,7 @@ static int launch_small(const FbCall &c, const SmallPlan &s, int G, unsigned *er
   for (int m = 0; m < c.nmat; ++m)
     if ((rc = api_tensor_map_u8(c.qw[m], c.K, c.N, c.K, 128, 128, &maps.w[m]))) return rc;
   FbParams p{c.sx, {c.sw[0], c.sw[1]}, static_cast<uint16_t *>(c.y),
-             static_cast<uint8_t *>(c.qh), c.sh, err, c.M, c.N, G, stages};
+             static_cast<uint8_t *>(c.qh), c.sh, err, c.M, c.N, G, stages, 0};
   void *args[] = {&maps, &p};
   const cudaError_t e = launch_kernel(
       fn, dim3(static_cast<unsigned>(s.blocks) * s.ks, s.tiles),
@@ -132,7 +132,7 @@ static int launch_large(const FbCall &c, const LargePlan &l, int G, int sms, uns
                                 &maps.w[m])))
       return rc;
   const FbParams p{c.sx, {c.sw[0], c.sw[1]}, static_cast<uint16_t *>(c.y),
-                   static_cast<uint8_t *>(c.qh), c.sh, err, c.M, c.N, G, 0};
+                   static_cast<uint8_t *>(c.qh), c.sh, err, c.M, c.N, G, 0, 0};
   const cudaError_t e = launch_fb_large(gate, l.pair, l.ks, maps, p, sms, st, api_pdl());
   if (e != cudaSuccess) return api_cuda_error(e, "block-scaled FP8 product launch");
   return DFK_OK;

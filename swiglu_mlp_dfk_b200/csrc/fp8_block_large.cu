@@ -9,8 +9,8 @@
 // 128: 32 KB of codes per CTA and group feed 512 tensor-core cycles.  For the
 // gated product CTA 0 brings 128 gate rows and CTA 1 the matching 128 up rows, so
 // each CTA holds both halves of 128 columns of h: one group of the quantised
-// output.  One persistent pair per two SMs walks the tiles in bands of FBL_BAND
-// token tiles, so that the tiles in flight share operands in L2.
+// output.  One persistent pair per two SMs walks the tiles in bands of token
+// tiles, so that the tiles in flight share operands in L2.
 //
 // Single: a CTA owns 128 tokens x 256 weight rows (48 KB per group); where there
 // are few tiles, clusters of 2 or 4 CTAs share a tile's groups and add their sums
@@ -49,7 +49,11 @@ constexpr int FBL_MAX_STAGES = 6;
 constexpr int FBL_PART_ROW = 1040;            // a token's 256 partial sums and 16 bytes
 constexpr int FBL_AHEAD = 8;       // groups whose scales are on the way (a power of two)
 constexpr int FBL_COMB = 4;        // groups whose s_x s_w are ready (a power of two)
-constexpr int FBL_BAND = 8;
+// A band of token tiles is as many as keep its activation codes, which every column
+// tile reads again, to a quarter of L2: the weights then come from HBM once a band.
+// Sustained, 8192 tokens, K = 4096, gated 8192: 576 us in bands of 8, 558 of 32;
+// K = N = 8192: 555 of 8, 553 of 16, 617 of 32.
+constexpr long long FBL_BAND_BYTES = 32 << 20;
 
 constexpr int FBL_OFF_OUT = FBL_RING;                      // 8 warps x 2 KB: output rows
 constexpr int FBL_OFF_SX = FBL_OFF_OUT + 8 * 2048;         // [AHEAD][128] s_x
@@ -162,16 +166,16 @@ __device__ __forceinline__ void cp_async_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-// Tile number -> (token tile, column tile): bands of FBL_BAND token tiles,
-// inside a band column tile by column tile.
+// Tile number -> (token tile, column tile): bands of token tiles, inside a band
+// column tile by column tile.
 struct FblTiles {
-  int tm, tn;
+  int tm, tn, band;
   __device__ __forceinline__ int count() const { return tm * tn; }
   __device__ __forceinline__ void at(int t, int &m, int &n) const {
-    const int band = t / (FBL_BAND * tn), r = t - band * FBL_BAND * tn;
-    const int h = min(FBL_BAND, tm - band * FBL_BAND);
+    const int b = t / (band * tn), r = t - b * band * tn;
+    const int h = min(band, tm - b * band);
     n = r / h;
-    m = band * FBL_BAND + (r - n * h);
+    m = b * band + (r - n * h);
   }
 };
 
@@ -240,7 +244,7 @@ __global__ void __launch_bounds__(FBL_THREADS, 1)
   const int m_cta = PAIR ? static_cast<int>(rank) * 128 : 0;  // this CTA's first in it
   const uint32_t lead = PAIR ? 0u : rank;          // the CTA that issues the MMAs
   const int NB = (p.N + 127) / 128;  // scale blocks along the weight rows
-  const FblTiles tiles{(p.M + TM - 1) / TM, GATE ? NB : (p.N + 255) / 256};
+  const FblTiles tiles{(p.M + TM - 1) / TM, GATE ? NB : (p.N + 255) / 256, p.band};
   const int ntiles = tiles.count();
   const int total = (ntiles - unit + nunits - 1) / nunits * nkb;  // groups of this CTA
 
@@ -650,6 +654,8 @@ cudaError_t launch_fb_large(bool gate, bool pair, int ks, const FbMaps &maps, co
   const long long units = ks > 1 ? tm * tn : std::min<long long>(sms / cluster, tm * tn);
   FbMaps mp = maps;
   FbParams pp = p;
+  const long long tile_bytes = static_cast<long long>(tokens) * p.G * FB_GROUP;
+  pp.band = static_cast<int>(std::min(64LL, std::max(4LL, FBL_BAND_BYTES / tile_bytes)));
   void *args[] = {&mp, &pp};
   return launch_kernel(fb_large_kernel_fn(gate, pair), dim3(static_cast<unsigned>(cluster * units)),
                        dim3(FBL_THREADS), FBL_SMEM, st, pdl, args,
