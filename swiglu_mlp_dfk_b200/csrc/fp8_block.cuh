@@ -37,7 +37,8 @@ struct FbScale {
 
 // v / b rounded to nearest, from b's correctly rounded reciprocal y and one
 // residual step (Markstein, "Computation of elementary functions on the IBM
-// RISC System/6000 processor", 1990): u = v y, u + (v - u b) y.  bf16 inputs
+// RISC System/6000 processor", 1990; for every b but one whose mantissa is all
+// ones): u = v y, u + (v - u b) y.  bf16 inputs
 // often make v / s a tie between two codes, so the plain product v y, off by
 // an ulp, would round a few codes in a thousand the other way.
 __device__ __forceinline__ float fb_divide(float v, float b, float y) {

@@ -25,8 +25,9 @@
 // barrier as the MMA.
 //
 // Measured (B200): 4096 tokens, K = 4096, gated, d_ff = 14336: 424 us in a burst
-// (2.27 PFLOP/s), 507 us for seconds on end (1.90, SM clock 1.4 GHz under the
-// 1000 W limit); K = 14336, N = 4096: 224 and 258 us.  On the way: one barrier per
+// (2.27 PFLOP/s), 490 us for seconds on end (1.97, SM clock 1.4 GHz under the
+// 1000 W limit); K = 14336, N = 4096: 214 and 254 us.  SiLU, the group maximum and
+// the codes of a tile take 5 % of it.  On the way: one barrier per
 // group instead of per half 524 us; loads of 32 TMEM columns instead of 16 680
 // cycles a group in place of 480 (the allocator copies registers); sixteen epilogue
 // warps of 64 sums no faster; single CTAs in place of pairs 14 % slower.
@@ -206,10 +207,11 @@ __device__ __forceinline__ void fbl_store_bf16(const FbParams &p, int m, int col
     if (DFK_IN_BOUNDS(col + 8 <= p.N, 31, p.err)) *reinterpret_cast<uint4 *>(at) = v;
     return;
   }
-  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-  for (int e = 0; e < 8; ++e)
-    if (col + e < p.N) at[e] = static_cast<uint16_t>(w[e >> 1] >> (16 * (e & 1)));
+  const uint64_t lo = v.x | static_cast<uint64_t>(v.y) << 32;
+  const uint64_t hi = v.z | static_cast<uint64_t>(v.w) << 32;
+#pragma unroll 1
+  for (int e = 0; e < min(8, p.N - col); ++e)
+    at[e] = static_cast<uint16_t>((e < 4 ? lo : hi) >> (16 * (e & 3)));
 }
 
 template <bool GATE, bool PAIR>

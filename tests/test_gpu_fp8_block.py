@@ -610,6 +610,9 @@ for M, K, N in ((1, 16, 1), (3, 2064, 1001), (33, 272, 96), (129, 1152, 640), (2
     t.test_gemm(M, K, N)
     t.test_gate_up(M, K, N, True)
     t.test_gate_up(M, K, N, False)
+t.test_forms_for_many_tokens(1100, 400, 5001, "gemm")
+t.test_forms_for_many_tokens(150, 4112, 2048, "fp8")
+t.test_forms_for_many_tokens(330, 144, 12296, "bf16")
 st = dfk.dfk_device_status()
 assert st[0] == 0, st
 print("checked ok")
