@@ -180,38 +180,53 @@ struct FblTiles {
   }
 };
 
-// 64 bytes of each of the warp's 32 rows (lane = row) to global memory, whole
-// 32-byte sectors a row: through 2 KB of shared memory, chunks of 16 bytes
-// swizzled so that neither side meets a bank twice.
-template <typename Store>
-__device__ __forceinline__ void fbl_rows64(uint8_t *buf, int lane, const uint32_t (&w)[16],
-                                           Store store) {
+// A warp's output goes to global memory through 2 KB of shared memory, so that
+// whole 32-byte sectors of a row are written together: 32 rows (lane = row) of 64
+// bytes, chunks of 16 bytes swizzled so that neither side meets a bank twice.
+__device__ __forceinline__ uint8_t *fbl_chunk(uint8_t *buf, int r, int c) {
+  return buf + r * 64 + ((c ^ ((r >> 1) & 3)) << 4);
+}
+
+__device__ __forceinline__ void fbl_stage(uint8_t *buf, int lane, const uint32_t (&w)[16]) {
 #pragma unroll
   for (int c = 0; c < 4; ++c)
-    *reinterpret_cast<uint4 *>(buf + lane * 64 + ((c ^ ((lane >> 1) & 3)) << 4)) =
+    *reinterpret_cast<uint4 *>(fbl_chunk(buf, lane, c)) =
         make_uint4(w[4 * c], w[4 * c + 1], w[4 * c + 2], w[4 * c + 3]);
-  __syncwarp();
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int r = 8 * i + (lane >> 2), c = lane & 3;
-    store(r, c, *reinterpret_cast<const uint4 *>(buf + r * 64 + ((c ^ ((r >> 1) & 3)) << 4)));
-  }
   __syncwarp();
 }
 
-// Eight bf16 of row m, columns col .. col + 7.
-__device__ __forceinline__ void fbl_store_bf16(const FbParams &p, int m, int col, const uint4 &v) {
-  if (m >= p.M || col >= p.N) return;
-  uint16_t *at = p.y + static_cast<size_t>(m) * p.N + col;
+// The staged rows m0 .. m0 + 31, columns n0 .. n0 + 31 of y: 16 bytes a lane where
+// the rows of y are aligned for it, else neighbouring lanes store neighbouring
+// pairs (N even) or elements of one row.
+__device__ __forceinline__ void fbl_store_bf16(const FbParams &p, uint8_t *buf, int lane, int m0,
+                                               int n0) {
   if ((p.N & 7) == 0) {
-    if (DFK_IN_BOUNDS(col + 8 <= p.N, 31, p.err)) *reinterpret_cast<uint4 *>(at) = v;
-    return;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int r = 8 * i + (lane >> 2), c = lane & 3, m = m0 + r, col = n0 + 8 * c;
+      const uint4 v = *reinterpret_cast<const uint4 *>(fbl_chunk(buf, r, c));
+      if (m < p.M && col < p.N && DFK_IN_BOUNDS(col + 8 <= p.N, 31, p.err))
+        *reinterpret_cast<uint4 *>(p.y + static_cast<size_t>(m) * p.N + col) = v;
+    }
+  } else if ((p.N & 1) == 0) {
+    const int e = 2 * (lane & 15), col = n0 + e;
+#pragma unroll 4
+    for (int r = lane >> 4; r < 32; r += 2) {
+      const uint32_t v =
+          *reinterpret_cast<const uint32_t *>(fbl_chunk(buf, r, e >> 3) + 2 * (e & 7));
+      if (m0 + r < p.M && col < p.N && DFK_IN_BOUNDS(col + 2 <= p.N, 36, p.err))
+        *reinterpret_cast<uint32_t *>(p.y + static_cast<size_t>(m0 + r) * p.N + col) = v;
+    }
+  } else {
+    const int col = n0 + lane;
+#pragma unroll 4
+    for (int r = 0; r < 32; ++r) {
+      const uint16_t v =
+          *reinterpret_cast<const uint16_t *>(fbl_chunk(buf, r, lane >> 3) + 2 * (lane & 7));
+      if (m0 + r < p.M && col < p.N) p.y[static_cast<size_t>(m0 + r) * p.N + col] = v;
+    }
   }
-  const uint64_t lo = v.x | static_cast<uint64_t>(v.y) << 32;
-  const uint64_t hi = v.z | static_cast<uint64_t>(v.w) << 32;
-#pragma unroll 1
-  for (int e = 0; e < min(8, p.N - col); ++e)
-    at[e] = static_cast<uint16_t>((e < 4 ? lo : hi) >> (16 * (e & 3)));
+  __syncwarp();
 }
 
 template <bool GATE, bool PAIR>
@@ -535,9 +550,8 @@ __global__ void __launch_bounds__(FBL_THREADS, 1)
             unpack_f32x2(acc[16 * c + e], lo, hi);
             w[e] = pack_bf16x2(lo, hi);
           }
-          fbl_rows64(obuf, lane, w, [&](int r, int cc, const uint4 &v) {
-            fbl_store_bf16(p, m0 + r, n0 + (c & 1) * 32 + (c >> 1) * 128 + 8 * cc, v);
-          });
+          fbl_stage(obuf, lane, w);
+          fbl_store_bf16(p, obuf, lane, m0, n0 + (c & 1) * 32 + (c >> 1) * 128);
         }
       } else {
         const int n0 = tn * 128 + 64 * half;
@@ -556,9 +570,8 @@ __global__ void __launch_bounds__(FBL_THREADS, 1)
             uint32_t w[16];
 #pragma unroll
             for (int e = 0; e < 16; ++e) w[e] = pack_bf16x2(h[32 * c + 2 * e], h[32 * c + 2 * e + 1]);
-            fbl_rows64(obuf, lane, w, [&](int r, int cc, const uint4 &v) {
-              fbl_store_bf16(p, m0 + r, n0 + 32 * c + 8 * cc, v);
-            });
+            fbl_stage(obuf, lane, w);
+            fbl_store_bf16(p, obuf, lane, m0, n0 + 32 * c);
           }
         } else {
           // the group's other 64 columns are in the warp with the same rows
@@ -580,11 +593,15 @@ __global__ void __launch_bounds__(FBL_THREADS, 1)
 #pragma unroll
           for (int e = 0; e < 16; ++e)
             w[e] = fb_codes4(h[4 * e], h[4 * e + 1], h[4 * e + 2], h[4 * e + 3], f);
-          fbl_rows64(obuf, lane, w, [&](int r, int cc, const uint4 &v) {
-            const int m = m0 + r, col = n0 + 16 * cc;
+          fbl_stage(obuf, lane, w);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int r = 8 * i + (lane >> 2), c = lane & 3, m = m0 + r, col = n0 + 16 * c;
+            const uint4 v = *reinterpret_cast<const uint4 *>(fbl_chunk(obuf, r, c));
             if (m < p.M && col < p.N && DFK_IN_BOUNDS(col + 16 <= p.N, 33, p.err))
               *reinterpret_cast<uint4 *>(p.qh + static_cast<size_t>(m) * p.N + col) = v;
-          });
+          }
+          __syncwarp();
           if (half == 0 && m0 + lane < p.M && DFK_IN_BOUNDS(tn < NB, 34, p.err))
             p.sh[static_cast<size_t>(tn) * p.M + m0 + lane] = f.s;
         }
