@@ -62,7 +62,8 @@ static SmallPlan plan_small(const FbCall &c, int G, int sms) {
   const int limit = s.pack ? 2 * sms : sms;
   s.ks = 1;
   while (s.ks < 8 && work * s.ks * 2 <= limit && s.ks * 8 <= G) s.ks *= 2;
-  s.us = 4.5 + 0.53 * ceil_div(G, s.ks) * ceil_div(work * s.ks, limit);
+  const int waves = ceil_div(work * s.ks, limit);
+  s.us = 1.9 + (2.6 + 0.53 * ceil_div(G, s.ks)) * waves;
   return s;
 }
 
@@ -78,21 +79,23 @@ struct LargePlan {
 static LargePlan plan_large(const FbCall &c, int G, int sms) {
   const long long tn = ceil_div(c.N, c.nmat == 2 ? 128 : 256);
   const long long singles = ceil_div(c.M, 128) * tn, pairs = ceil_div(c.M, 256) * tn;
-  LargePlan best{true, 1, 6.0 + 0.36 * G * ceil_div(pairs, sms / 2)};
+  LargePlan best{true, 1, 4.0 + (2.0 + 0.36 * G) * ceil_div(pairs, sms / 2)};
   for (int ks = 1; ks <= 4 && ks * 4 <= std::max(G, 4); ks *= 2) {
     if (ks > 1 && singles * ks > sms * 9 / 10) break;
     const double us =
-        (ks > 1 ? 10.0 : 6.0) + 0.42 * ceil_div(G, ks) * ceil_div(singles * ks, sms);
+        (ks > 1 ? 8.0 : 4.0) + (2.0 + 0.42 * ceil_div(G, ks)) * ceil_div(singles * ks, sms);
     if (us < best.us) best = LargePlan{false, ks, us};
   }
   return best;
 }
 
-// `us` above: what a call takes, fitted to 30 shapes of 48 to 4096 tokens on a
-// B200: a fixed part (launch, first loads, output; 4 us more where a cluster adds
-// its shares) and a part per group and round of tiles.  Both sides at 192 tokens:
+// `us` above: what a call takes, fitted to 60 shapes of 48 to 8192 tokens on a
+// B200: a fixed part (launch, first loads; 4 us more where a cluster adds its
+// shares), a part per round of tiles (their output, which the next tile's groups
+// do not hide) and a part per group of a round.  Both sides at 192 tokens:
 // N = 6144, K = 4096 14.0 us streaming, 17.8 by pairs; N = 4096, K = 14336 33.6 us
 // streaming, 23.1 by clusters of 4, 46.5 by pairs; N = 16384, K = 4096 41, 21.5, 20.
+// 8192 tokens, N = 1024, K = 128: 13.6 streaming, 9.4 by pairs, 9.7 by single CTAs.
 static int launch_small(const FbCall &c, const SmallPlan &s, int G, unsigned *err,
                         cudaStream_t st) {
   if (s.tiles > 65535) return api_fail(DFK_ERR_UNSUPPORTED_SHAPE, "M=%d is too large", c.M);

@@ -267,7 +267,8 @@ def test_gate_up(M, D, F, fp8_out):
 # Sizes of the tensor-bound kernel's forms: pairs of CTAs, single CTAs (fewer rounds of tiles),
 # clusters that share a tile's groups; odd columns, part tiles, shorter last groups.
 @pytest.mark.parametrize("M,K,N", [(1100, 400, 5001), (2300, 272, 4112), (400, 272, 9008),
-                                   (330, 144, 12296), (192, 14336, 4001), (150, 4112, 2048)])
+                                   (330, 144, 12296), (192, 14336, 4001), (150, 4112, 2048),
+                                   (700, 656, 3002)])
 @pytest.mark.parametrize("op", ["gemm", "fp8", "bf16"])
 def test_forms_for_many_tokens(M, K, N, op):
     g = gen(M + K)
@@ -612,6 +613,7 @@ for M, K, N in ((1, 16, 1), (3, 2064, 1001), (33, 272, 96), (129, 1152, 640), (2
     t.test_gate_up(M, K, N, False)
 t.test_forms_for_many_tokens(1100, 400, 5001, "gemm")
 t.test_forms_for_many_tokens(150, 4112, 2048, "fp8")
+t.test_forms_for_many_tokens(700, 656, 3002, "gemm")
 t.test_forms_for_many_tokens(330, 144, 12296, "bf16")
 st = dfk.dfk_device_status()
 assert st[0] == 0, st
