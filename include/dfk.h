@@ -268,14 +268,15 @@ DFK_API int dfk_rmsnorm_qkv_proj(const void *x, const void *gamma, float eps,
  *
  * Shared rules: 0 <= M (no upper limit of 64 here; M == 0 is a no-op
  * returning DFK_OK); K, and the row length of a quantised output, a multiple
- * of 16; any N otherwise.  Codes, bf16 tensors: 16-byte aligned; scales: 4-byte
+ * of 16; any N otherwise; every size at most 2^31 - 1024.  Codes, bf16 tensors: 16-byte aligned; scales: 4-byte
  * aligned.  Sums are fp32: exact products of codes, summed per group by
  * the tensor core, scaled by s_x s_w and added in fp32 in a fixed order (the
  * same bits on every call).  No workspace and no allocation: calls may run on
  * several streams at once and be captured in graphs.  Inputs and outputs must
  * not overlap, except residual_out with x or residual (the same pointer).
  * Weights, their scales and gamma are read before the previous kernel in
- * the stream has finished, as above.
+ * the stream has finished, as above: codes that dfk_quant_fp8_block has just
+ * written are activations, and weights only after a synchronisation.
  */
 
 /* q, s = the codes and scales of x [M][K] bf16. */

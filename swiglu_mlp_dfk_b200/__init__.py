@@ -365,6 +365,7 @@ _BF16_ONLY = (_BF16,)
 _F32 = torch.float32
 _F32_ONLY = (_F32,)
 _Tensor = torch.Tensor
+_INT_END = 1 << 31  # sizes travel as C ints
 _get_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 
@@ -389,6 +390,9 @@ def _fb_rows(name, t):
     if not isinstance(t, _Tensor) or t.dim() != 2 or not t.is_cuda:
         raise DfkError(DFK_ERR_INVALID_ARG, "%s must be a 2-D CUDA tensor" % name)
     shape = t.shape
+    if max(shape) >= _INT_END:
+        raise DfkError(DFK_ERR_UNSUPPORTED_SHAPE, "%s %s: a size is too large"
+                       % (name, tuple(shape)))
     return shape[0], shape[1], t.get_device()
 
 
@@ -401,7 +405,7 @@ def _fb_activations(name, t):
     try:
         M, K = t.shape
         dev = t.get_device()
-        if t.dtype is _BF16 and dev >= 0 and t.is_contiguous():
+        if t.dtype is _BF16 and dev >= 0 and t.is_contiguous() and M | K < _INT_END:
             return M, K, dev
     except (AttributeError, TypeError, ValueError):
         pass
@@ -421,7 +425,7 @@ def _fb_operands(q_x, s_x, q_w, s_w, name):
                 and s_w.shape == ((N + 127) >> 7, G)
                 and 0 <= dev == s_x.get_device() == q_w.get_device() == s_w.get_device()
                 and q_x.is_contiguous() and s_x.is_contiguous() and q_w.is_contiguous()
-                and s_w.is_contiguous()):
+                and s_w.is_contiguous() and M | N | K < _INT_END):
             return M, K, N, G, dev
     except (AttributeError, TypeError, ValueError):
         pass
@@ -511,7 +515,9 @@ def dfk_add_rmsnorm_fp8_block(x, residual, gamma, eps, residual_out=None, q=None
 def dfk_gemm_fp8_block(q_x, s_x, q_w, s_w, y=None, stream=None):
     """y = x W^T, x in block-scaled FP8 (q_x [M, K], s_x [ceil(K/128), M]), W as E4M3 codes
     q_w [N, K] with one fp32 scale per 128 x 128 block, s_w [ceil(N/128), ceil(K/128)];
-    returns y [M, N] bf16."""
+    returns y [M, N] bf16.  Weights are read before the previous call on the stream has
+    finished: codes that dfk_quant_fp8_block has just written are no q_w without a
+    synchronisation in between."""
     M, K, N, _, dev = _fb_operands(q_x, s_x, q_w, s_w, "q_w")
     if y is None:
         y = torch.empty(M, N, dtype=_BF16, device=s_x.device)

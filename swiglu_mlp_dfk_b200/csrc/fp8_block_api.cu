@@ -15,8 +15,13 @@ namespace dfk {
 static bool off16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) != 0; }
 static bool off4(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 3u) != 0; }
 
+// Sizes the kernels' 32-bit coordinates hold with a tile to spare.
+constexpr int FB_MAX_SIZE = 0x7fffffff - 1023;
+
 static int check_rows(int M, int K) {
   if (M < 0 || K <= 0) return api_fail(DFK_ERR_INVALID_ARG, "negative or zero size");
+  if (M > FB_MAX_SIZE || K > FB_MAX_SIZE)
+    return api_fail(DFK_ERR_UNSUPPORTED_SHAPE, "%d x %d: a size is too large", M, K);
   if (K % 16) return api_fail(DFK_ERR_UNSUPPORTED_SHAPE, "row length %% 16 != 0 (%d)", K);
   return DFK_OK;
 }
@@ -145,6 +150,8 @@ static int product(const FbCall &c, cudaStream_t st) {
   int rc = check_rows(c.M, c.K);
   if (rc) return rc;
   if (c.N <= 0) return api_fail(DFK_ERR_INVALID_ARG, "negative or zero size");
+  if (c.N > FB_MAX_SIZE)
+    return api_fail(DFK_ERR_UNSUPPORTED_SHAPE, "%d weight rows: too large", c.N);
   if (c.qh || c.sh) {
     if (c.y) return api_fail(DFK_ERR_INVALID_ARG, "both a bf16 and a quantised output");
     if (c.N % 16)

@@ -59,6 +59,10 @@ def gate_up(L, qx=P, sx=P2, qg=P3, sg=P4, qu=P3, su=P4, h=None, qh=P5, sh=P6, M=
     (gate_up, dict(qu=None), BAD), (gate_up, dict(su=None), BAD), (gate_up, dict(qg=MIS), ALIGN),
     (gate_up, dict(qu=MIS), ALIGN), (gate_up, dict(qh=MIS), ALIGN), (gate_up, dict(sh=ODD), ALIGN),
     (gate_up, dict(su=ODD), ALIGN), (gate_up, dict(h=MIS, qh=None, sh=None), ALIGN),
+    (quant, dict(M=2 ** 31 - 1), SHAPE), (quant, dict(K=2 ** 31 - 16), SHAPE),
+    (norm, dict(M=2 ** 31 - 1), SHAPE), (gemm, dict(M=2 ** 31 - 1), SHAPE),
+    (gemm, dict(K=2 ** 31 - 16), SHAPE), (gemm, dict(N=2 ** 31 - 1), SHAPE),
+    (gate_up, dict(F=2 ** 31 - 16), SHAPE),
 ])
 def test_refusals(L, fn, kw, status):
     assert fn(L, **kw) == status

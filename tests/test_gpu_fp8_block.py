@@ -596,6 +596,20 @@ def test_binding_refusals():
         dfk.dfk_swiglu_gate_up_fp8_block(q, s, qw, sw, qw, sw, fp8_out=False, q_h=q)
 
 
+def test_sizes_beyond_a_c_int_are_refused():
+    # 2^32 + 16 would arrive as 16
+    x = torch.empty(1, 2 ** 32 + 16, device="cuda", dtype=torch.uint8)
+    s = torch.empty(2 ** 25 + 1, 1, device="cuda")
+    sw = torch.empty(1, 2 ** 25 + 1, device="cuda")
+    for call in (lambda: dfk.dfk_gemm_fp8_block(x, s, x, sw),
+                 lambda: dfk.dfk_swiglu_gate_up_fp8_block(x, s, x, sw, x, sw),
+                 lambda: dfk.dfk_quant_fp8_block(torch.empty(1, 2 ** 32 + 16, device="cuda",
+                                                             dtype=torch.bfloat16))):
+        with pytest.raises(dfk.DfkError) as e:
+            call()
+        assert e.value.status == dfk.DFK_ERR_UNSUPPORTED_SHAPE
+
+
 CHILD = r'''
 import os, sys
 sys.path.insert(0, os.environ["DFK_ROOT"])
