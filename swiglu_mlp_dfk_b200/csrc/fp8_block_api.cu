@@ -51,6 +51,10 @@ static int ceil_div(long long a, long long b) { return static_cast<int>((a + b -
 // 9.1 at one CTA; clusters of 3, as many as fill the SMs, 15.5: they do not all
 // fit at once).  Two matrices: one CTA on an SM with all of its shared memory
 // (stages of 32 KB and more), two where the row blocks outnumber the SMs.
+// Clusters of 8 that have their SMs to themselves find room on three quarters of
+// them, no more (K = 4096, 1 token: d_ff = 1920 7.4 us, 2048 12.1, 7.2 in clusters of 4), and
+// above 16 tokens their meeting costs more than four groups less (24 tokens, d_ff =
+// 1024: K = 4096 8.5 us, 7.8 in clusters of 4; K = 8192 10.4 and 11.0).
 struct SmallPlan {
   int bn, blocks, tiles, ks;
   bool pack;
@@ -67,6 +71,7 @@ static SmallPlan plan_small(const FbCall &c, int G, int sms) {
   const int limit = s.pack ? 2 * sms : sms;
   s.ks = 1;
   while (s.ks < 8 && work * s.ks * 2 <= limit && s.ks * 8 <= G) s.ks *= 2;
+  if (!s.pack && s.ks == 8 && (work * 8 > sms * 3 / 4 || (s.bn > 16 && G < 64))) s.ks = 4;
   const int waves = ceil_div(work * s.ks, limit);
   s.us = 1.9 + (2.6 + 0.53 * ceil_div(G, s.ks)) * waves;
   return s;
