@@ -266,6 +266,9 @@ __global__ void __launch_bounds__(FBL_THREADS, 1)
   const int total = (ntiles - unit + nunits - 1) / nunits * nkb;  // groups of this CTA
 
   if (tid == 0) {
+    tensormap_prefetch(&maps.w[0]);
+    if (GATE) tensormap_prefetch(&maps.w[1]);
+    tensormap_prefetch(&maps.x);
     for (int s = 0; s < S; ++s) {
       mbar_init(&fullb[s], 1);
       mbar_init(&empty[s], 1);
@@ -302,12 +305,34 @@ __global__ void __launch_bounds__(FBL_THREADS, 1)
     // (PAIR) or all 256: 64 rows of each half after the other
     if (lane == 0) {
       const uint64_t pol = l2_policy_evict_normal();
+      auto load_w = [&](int kb, int st, int tn) {
+        uint8_t *sb = smem + st * STAGE + FBL_HALF;
+        if constexpr (PAIR) {
+          if (rank == 0) mbar_arrive_expect_tx(&fullb[st], 2 * STAGE);
+          const CUtensorMap *wmap = GATE && rank ? &maps.w[1] : &maps.w[0];
+          const int wrow = GATE ? tn * 128 : tn * 256 + static_cast<int>(rank) * 128;
+          tma_load_2d_pair(sb, wmap, cluster_map(smem_addr(&fullb[st]), 0), kb * 128, wrow, pol);
+        } else {
+          mbar_arrive_expect_tx(&fullb[st], STAGE);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {  // half i / 2, matrix or 128-row block i % 2
+            const int wrow = (GATE ? tn * 128 : tn * 256 + 128 * (i & 1)) + 64 * (i >> 1);
+            tma_load_2d(sb + i * (FBL_HALF / 2), &maps.w[GATE ? i & 1 : 0], &fullb[st], kb * 128,
+                        wrow, pol);
+          }
+        }
+      };
+      // the first stages' weights, before the dependency on the previous kernel (a
+      // layer of norm, gate/up and down, 96 tokens, 4096 x 14336: 49.5 -> 48.9 us)
+      const int early = min(S, nkb);
+      int tm, tn;
+      tiles.at(unit, tm, tn);
+      for (int i = 0; i < early; ++i) load_w(kb0 + i, i, tn);
       pdl_wait();
       int it = 0, st = 0;
       uint32_t ph = 0;
       bool ok = true;
       for (int t = unit; ok && t < ntiles; t += nunits) {
-        int tm, tn;
         tiles.at(t, tm, tn);
         const int mrow = tm * TM + m_cta;
         for (int kb = kb0; kb < kb0 + nkb; ++kb, ++it) {
@@ -315,24 +340,12 @@ __global__ void __launch_bounds__(FBL_THREADS, 1)
             ok = false;
             break;
           }
-          uint8_t *sb = smem + st * STAGE;
-          if constexpr (PAIR) {
-            if (rank == 0) mbar_arrive_expect_tx(&fullb[st], 2 * STAGE);
-            const uint32_t bar = cluster_map(smem_addr(&fullb[st]), 0);
-            const CUtensorMap *wmap = GATE && rank ? &maps.w[1] : &maps.w[0];
-            const int wrow = GATE ? tn * 128 : tn * 256 + static_cast<int>(rank) * 128;
-            tma_load_2d_pair(sb, &maps.x, bar, kb * 128, mrow, pol);
-            tma_load_2d_pair(sb + FBL_HALF, wmap, bar, kb * 128, wrow, pol);
-          } else {
-            mbar_arrive_expect_tx(&fullb[st], STAGE);
-            tma_load_2d(sb, &maps.x, &fullb[st], kb * 128, mrow, pol);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {  // half i / 2, matrix or 128-row block i % 2
-              const int wrow = (GATE ? tn * 128 : tn * 256 + 128 * (i & 1)) + 64 * (i >> 1);
-              tma_load_2d(sb + FBL_HALF + i * (FBL_HALF / 2), &maps.w[GATE ? i & 1 : 0],
-                          &fullb[st], kb * 128, wrow, pol);
-            }
-          }
+          if (it >= early) load_w(kb, st, tn);
+          if constexpr (PAIR)
+            tma_load_2d_pair(smem + st * STAGE, &maps.x, cluster_map(smem_addr(&fullb[st]), 0),
+                             kb * 128, mrow, pol);
+          else
+            tma_load_2d(smem + st * STAGE, &maps.x, &fullb[st], kb * 128, mrow, pol);
           if (++st == S) {
             st = 0;
             ph ^= 1u;
