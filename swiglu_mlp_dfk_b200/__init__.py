@@ -17,6 +17,7 @@ variants.
 import ctypes
 import os
 import threading
+import warnings
 
 import torch
 
@@ -96,6 +97,7 @@ class dfk_variant(ctypes.Structure):
 
 
 _lib = None
+_fast = None  # _dfk_torch.so, bound to the loaded library
 _lock = threading.Lock()
 
 
@@ -159,8 +161,24 @@ def lib():
             L.dfk_mlp_stack_workspace_bytes.restype = ll
             L.dfk_clear_variant_cache.argtypes = []
             L.dfk_clear_variant_cache.restype = None
+            _load_calls(L)
             _lib = L
     return _lib
+
+
+def _load_calls(L):
+    """Bind csrc/torch_calls.cpp to the library's block-scaled entry points."""
+    global _fast
+    try:
+        from . import _dfk_torch
+    except ImportError as e:
+        warnings.warn("_dfk_torch.so cannot be loaded (%s): calls of the block-scaled FP8 "
+                      "operators take 3-7 us more on the host" % e, RuntimeWarning)
+        return
+    _dfk_torch.bind(*(ctypes.cast(fn, ctypes.c_void_p).value for fn in (
+        L.dfk_quant_fp8_block, L.dfk_add_rmsnorm_fp8_block, L.dfk_gemm_fp8_block,
+        L.dfk_swiglu_gate_up_fp8_block)))
+    _fast = _dfk_torch
 
 
 def _check(status):
@@ -396,9 +414,11 @@ def _fb_rows(name, t):
     return shape[0], shape[1], t.get_device()
 
 
-# A call on a small tensor is bound by its Python (a launch takes 3 us, the kernels 1-2): the
-# entry points test their operands in one expression of attribute reads (0.1 us each) and go
-# through the checks above, which name the fault, only where it fails.
+# A call on a small tensor is bound by its host side (a launch takes 3 us, the kernels 1-2): the
+# entry points first try csrc/torch_calls.cpp, which makes the usual call as a whole.  Where it
+# does not (None: a stream given, another device, an argument to refuse) the operands are
+# tested in one expression of attribute reads (0.1 us each) and go through the checks above,
+# which name the fault, only where it fails.
 
 def _fb_activations(name, t):
     """(M, K, device index) of a bf16 activation tensor."""
@@ -480,6 +500,10 @@ def _fb_codes_out(q, s, M, K, dev, stream, device):
 def dfk_quant_fp8_block(x, q=None, s=None, stream=None):
     """Block-scaled FP8 of x [M, K] bf16: returns (q [M, K] float8_e4m3fn, s [ceil(K/128), M]
     fp32), s = max(max|x| / 448, 2^-126) per token and group of 128, q = E4M3(x / s)."""
+    if stream is None and _fast is not None:
+        out = _fast.quant(x, q, s)
+        if out is not None:
+            return out
     M, K, dev = _fb_activations("x", x)
     q, s = _fb_codes_out(q, s, M, K, dev, stream, x.device)
     _fb_call(dev, stream, (_lib or lib()).dfk_quant_fp8_block, x.data_ptr(), q.data_ptr(),
@@ -492,6 +516,10 @@ def dfk_add_rmsnorm_fp8_block(x, residual, gamma, eps, residual_out=None, q=None
     """r = bf16(x + residual) (r = x for residual None), then the block-scaled FP8 of
     RMSNorm(r; gamma, eps): returns (q, s, r), r None without a residual.  residual_out may be
     `residual` or `x` itself: the sum is then kept in place."""
+    if stream is None and _fast is not None:
+        out = _fast.norm(x, residual, gamma, eps, residual_out, q, s)
+        if out is not None:
+            return out
     M, D, dev = _fb_activations("x", x)
     _fb_check("gamma", gamma, _BF16_ONLY, (D,), dev)
     p_res = p_out = None
@@ -518,6 +546,10 @@ def dfk_gemm_fp8_block(q_x, s_x, q_w, s_w, y=None, stream=None):
     returns y [M, N] bf16.  Weights are read before the previous call on the stream has
     finished: codes that dfk_quant_fp8_block has just written are no q_w without a
     synchronisation in between."""
+    if stream is None and _fast is not None:
+        out = _fast.gemm(q_x, s_x, q_w, s_w, y)
+        if out is not None:
+            return out
     M, K, N, _, dev = _fb_operands(q_x, s_x, q_w, s_w, "q_w")
     if y is None:
         y = torch.empty(M, N, dtype=_BF16, device=s_x.device)
@@ -535,6 +567,10 @@ def dfk_swiglu_gate_up_fp8_block(q_x, s_x, q_gate, s_gate, q_up, s_up, fp8_out=T
     """h = SiLU(x W_gate^T) * (x W_up^T) in one kernel, operands as for dfk_gemm_fp8_block
     (W_gate, W_up [d_ff, d_model]).  fp8_out: returns (q_h, s_h), h in block-scaled FP8 from its
     fp32 values; otherwise returns h [M, d_ff] bf16."""
+    if stream is None and _fast is not None:
+        out = _fast.gate_up(q_x, s_x, q_gate, s_gate, q_up, s_up, fp8_out, h, q_h, s_h)
+        if out is not None:
+            return out
     M, D, F, G, dev = _fb_operands(q_x, s_x, q_gate, s_gate, "q_gate")
     _fb_check("q_up", q_up, _FP8_CODES, (F, D), dev)
     _fb_check("s_up", s_up, _F32_ONLY, ((F + 127) >> 7, G), dev)

@@ -14,6 +14,9 @@ and the activation loads test their index against the tensor's extent and
 record the first failure in the device status word instead of accessing
 memory) goes to ``_build/checked/`` and ``swiglu_mlp_dfk_b200/libdfk_checked.so``;
 the binding loads it when ``DFK_CHECKED=1`` is set.
+
+``_dfk_torch.so`` (csrc/torch_calls.cpp, g++) holds the host side of the block-scaled
+FP8 calls for the Python binding; libdfk.so does not need it.
 """
 import concurrent.futures as cf
 import os
@@ -27,6 +30,8 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libdfk.so")
 LIB_CHECKED = os.path.join(PKG, "libdfk_checked.so")
+LIB_CALLS = os.path.join(PKG, "_dfk_torch.so")
+CALLS_SRC = os.path.join(CSRC, "torch_calls.cpp")
 
 NVCC = os.environ.get("NVCC", "nvcc")
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
@@ -86,14 +91,41 @@ def _build_one(lib, outdir, extra, force, jobs, verbose):
     return lib
 
 
+def _build_calls(force, verbose):
+    """Compile csrc/torch_calls.cpp, a Python module over torch's C++ API, with g++."""
+    header = os.path.join(INCLUDE, "dfk.h")
+    if (not force and os.path.exists(LIB_CALLS)
+            and os.path.getmtime(LIB_CALLS) >= _newest([CALLS_SRC, header])):
+        return
+    import sysconfig
+
+    import torch
+    from torch.utils.cpp_extension import include_paths, library_paths
+    tmp = LIB_CALLS + ".tmp.%d" % os.getpid()
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared",
+           "-fvisibility=hidden", "-D_GLIBCXX_USE_CXX11_ABI=%d" % torch._C._GLIBCXX_USE_CXX11_ABI,
+           "-I", INCLUDE, "-I", sysconfig.get_paths()["include"]]
+    cmd += [x for p in include_paths("cuda") for x in ("-isystem", p)]
+    cmd += [CALLS_SRC, "-o", tmp] + ["-L" + p for p in library_paths("cuda")]
+    cmd += ["-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError("g++ failed:\n%s\n%s%s" % (" ".join(cmd), r.stdout, r.stderr))
+    os.replace(tmp, LIB_CALLS)
+    if verbose:
+        print(LIB_CALLS)
+
+
 def build(force: bool = False, jobs: int = 0, verbose: bool = False,
           checked: bool = True) -> str:
     """Compile every .cu under csrc/ and link libdfk.so (and, with `checked`,
-    the bounds-checked libdfk_checked.so); returns the path of libdfk.so."""
+    the bounds-checked libdfk_checked.so), and _dfk_torch.so; returns the path of
+    libdfk.so."""
     lib = _build_one(LIB, BUILD, [], force, jobs, verbose)
     if checked:
         _build_one(LIB_CHECKED, os.path.join(BUILD, "checked"), ["-DDFK_CHECKED"], force, jobs,
                    verbose)
+    _build_calls(force, verbose)
     return lib
 
 

@@ -93,6 +93,15 @@ def test_binding_refuses_host_tensors():
         assert e.value.status == BAD
 
 
+def test_fast_calls_refuse_quietly(L):
+    x = torch.zeros(2, 128, dtype=torch.bfloat16)
+    f = dfk._fast
+    for call, n in ((f.quant, 3), (f.norm, 7), (f.gemm, 5), (f.gate_up, 10)):
+        for v in (x, None, 1, 1.0, "x", [x]):
+            assert call(*[v] * n) is None
+        assert call() is None and call(*[x] * (n + 1)) is None
+
+
 @pytest.mark.parametrize("N,K", [(1, 16), (128, 128), (129, 144), (300, 272)])
 def test_weight_encoder(N, K):
     g = torch.Generator().manual_seed(N)

@@ -610,6 +610,116 @@ def test_sizes_beyond_a_c_int_are_refused():
         assert e.value.status == dfk.DFK_ERR_UNSUPPORTED_SHAPE
 
 
+def every_call(q, s, w, x, gamma):
+    """One call of each kind: with new outputs, given ones, bf16 and codes, no tokens."""
+    u8 = torch.uint8
+    M, K = x.shape
+    N = w[0][0].shape[0]
+    yield dfk.dfk_quant_fp8_block(x)
+    qo, so = torch.empty(M, K, device="cuda", dtype=u8), torch.empty(-(-K // 128), M, device="cuda")
+    out = dfk.dfk_quant_fp8_block(x, q=qo, s=so)
+    assert out[0] is qo and out[1] is so
+    yield out
+    yield dfk.dfk_quant_fp8_block(x[:0])
+    yield dfk.dfk_add_rmsnorm_fp8_block(x, None, gamma, 1e-5)
+    yield dfk.dfk_add_rmsnorm_fp8_block(x, x, gamma, 0)
+    r = x.clone()
+    out = dfk.dfk_add_rmsnorm_fp8_block(x, r, gamma, 1e-5, residual_out=r)
+    assert out[2] is r
+    yield out
+    yield (dfk.dfk_gemm_fp8_block(q, s, *w[0]),)
+    yield (dfk.dfk_gemm_fp8_block(q.view(u8), s, w[0][0].view(u8), w[0][1]),)
+    y = torch.empty(M, N, device="cuda", dtype=torch.bfloat16)
+    assert dfk.dfk_gemm_fp8_block(q, s, *w[0], y=y) is y
+    yield (y,)
+    yield dfk.dfk_swiglu_gate_up_fp8_block(q, s, *w[0], *w[1])
+    yield (dfk.dfk_swiglu_gate_up_fp8_block(q, s, *w[0], *w[1], fp8_out=False),)
+    qh, sh = torch.empty(M, N, device="cuda", dtype=u8), torch.empty(-(-N // 128), M, device="cuda")
+    out = dfk.dfk_swiglu_gate_up_fp8_block(q, s, *w[0], *w[1], q_h=qh, s_h=sh)
+    assert out[0] is qh and out[1] is sh
+    yield out
+
+
+@pytest.mark.parametrize("M", [1, 5, 70])
+def test_both_host_paths_make_the_same_calls(M, monkeypatch):
+    dfk.lib()
+    assert dfk._fast is not None
+    g = gen(M)
+    q, s = activations(g, M, 272)
+    w = weights(g, 400, 272), weights(g, 400, 272)
+    x = torch.randn(M, 272, device="cuda", dtype=torch.bfloat16)
+    gamma = torch.rand(272, device="cuda").bfloat16()
+
+    def run():
+        return [tuple(t if t is None else t.clone() for t in out)
+                for out in every_call(q, s, w, x, gamma)]
+    fast = run()
+    with torch.inference_mode():
+        inside = run()
+    monkeypatch.setattr(dfk, "_fast", None)
+    plain = run()
+    for a, b, c in zip(fast, plain, inside):
+        assert len(a) == len(b) == len(c)
+        for t, u, v in zip(a, b, c):
+            assert (t is None) == (u is None) == (v is None)
+            if t is not None:
+                assert t.dtype == u.dtype and t.shape == u.shape and t.stride() == u.stride()
+                assert t.numel() == 0 or (torch.equal(t.view(torch.uint8), u.view(torch.uint8))
+                                          and torch.equal(t.view(torch.uint8), v.view(torch.uint8)))
+
+
+def test_fast_calls_leave_the_unusual_to_the_binding():
+    g = gen(3)
+    q, s = activations(g, 4, 256)
+    qw, sw = weights(g, 128, 256)
+    x = torch.randn(4, 256, device="cuda", dtype=torch.bfloat16)
+    gamma = torch.ones(256, device="cuda", dtype=torch.bfloat16)
+    dfk.lib()
+    f = dfk._fast
+    y = f.gemm(q, s, qw, sw, None)
+    assert torch.equal(y, dfk.dfk_gemm_fp8_block(q, s, qw, sw))
+    for args in ((q.cpu(), s, qw, sw, None), (q, s.t(), qw, sw, None), (q, s, qw.t(), sw, None),
+                 (q, s, qw, sw[:, :1], None), (q, s, qw, sw, y[:3]), (q, s, qw, sw, y.float()),
+                 (q.float(), s, qw, sw, None), (q[0], s, qw, sw, None), (q, s, qw, sw),
+                 (q, s, None, sw, None), (q, s.double(), qw, sw, None), (q, s, qw, 1.0, None)):
+        assert f.gemm(*args) is None
+    for args in ((x.float(), None, None), (x.t(), None, None), (x[:, :200].contiguous(), None, None),
+                 (x, q[:2], None), (x, None, s.t()), (x, x, None), (x.cpu(), None, None)):
+        assert f.quant(*args) is None
+    for args in ((x, x, gamma[:128], 1e-5, None, None, None), (x, x[:2], gamma, 1e-5, None, None, None),
+                 (x, None, gamma, 1e-5, x, None, None), (x, x, gamma, 1, None, None, None),
+                 (x, x, gamma, -1.0, None, None, None), (x, x, x, 1e-5, None, None, None)):
+        assert f.norm(*args) is None
+    for args in ((q, s, qw, sw, qw[:64], sw, True, None, None, None),
+                 (q, s, qw, sw, qw, sw, True, y, None, None), (q, s, qw, sw, qw, sw, 1, None, None, None),
+                 (q, s, qw, sw, qw, sw, False, None, q, None)):
+        assert f.gate_up(*args) is None
+
+
+def test_calls_from_several_threads():
+    import threading
+    g = gen(9)
+    q, s = activations(g, 33, 512)
+    w = weights(g, 384, 512)
+    want = dfk.dfk_gemm_fp8_block(q, s, *w)
+    torch.cuda.synchronize()
+    wrong = []
+
+    def work():
+        with torch.cuda.stream(torch.cuda.Stream()):
+            for _ in range(200):
+                y = dfk.dfk_gemm_fp8_block(q, s, *w)
+            torch.cuda.current_stream().synchronize()
+            if not torch.equal(y, want):
+                wrong.append(1)
+    ts = [threading.Thread(target=work) for _ in range(4)]
+    for t in ts:
+        t.start()
+    for t in ts:
+        t.join()
+    assert not wrong
+
+
 CHILD = r'''
 import os, sys
 sys.path.insert(0, os.environ["DFK_ROOT"])
