@@ -171,8 +171,9 @@ __global__ void __launch_bounds__(1024)
   const float t = __uint_as_float((rb & 0x007fffffu) | 0x3f800000u);
   // r = c t, c a power of two and t in [1, 2): u = (a c) gamma is exact (a
   // product of two bf16 factors), and t falls out of v / s, so that the codes
-  // depend on no rounding but that of 448 / max |u| -- unless the scale is at
-  // its floor.
+  // depend on no rounding but that of max |u| / 448.  Not so where the floor or
+  // an overflow to infinity parts the scales of u and of v = u t: there v itself,
+  // rounded, is divided by the stored scale.
   float u[CPT][8], top[CPT];
 #pragma unroll
   for (int i = 0; i < CPT; ++i) {
@@ -199,9 +200,9 @@ __global__ void __launch_bounds__(1024)
   for (int i = 1; i < CPT; ++i) mine = li == i ? top[i] : mine;
   const float s_v = fb_group_scale(mine * t);
   float s_u = fb_group_scale(mine);
-  if (s_v == 1.17549435e-38f) s_u = s_v / t;
-  if (s_v != s_v) s_u = s_v;
-  const float inv = 1.0f / s_u;
+  // its sign tells the group's lanes that they divide v, not u, by it
+  if (!(s_u > 1.17549435e-38f && s_v <= 3.402823466e38f)) s_u = -s_v;
+  const float inv = 1.0f / fabsf(s_u);
   {
     const int k = 8 * (tid - l + T * li);  // the group's first element
     if (l < CPT && k < D && DFK_IN_BOUNDS(k / FB_GROUP < G && m < M, 26, err))
@@ -210,8 +211,12 @@ __global__ void __launch_bounds__(1024)
 #pragma unroll
   for (int i = 0; i < CPT; ++i) {
     const int k = 8 * (tid + T * i);
-    const FbScale f = fb_scale_of(__shfl_sync(0xffffffffu, s_u, i, 16),
-                                  __shfl_sync(0xffffffffu, inv, i, 16));
+    const float su = __shfl_sync(0xffffffffu, s_u, i, 16);
+    const FbScale f = fb_scale_of(fabsf(su), __shfl_sync(0xffffffffu, inv, i, 16));
+    if (su < 0.f) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) u[i][j] *= t;
+    }
     if (k < D && DFK_IN_BOUNDS(k + 8 <= D && m < M, 25, err))
       *reinterpret_cast<uint2 *>(q + row + k) =
           make_uint2(fb_codes4(u[i][0], u[i][1], u[i][2], u[i][3], f),

@@ -229,6 +229,38 @@ def test_add_rmsnorm_all_zero_row_with_zero_eps_is_nan_as_the_formula():
     assert torch.isfinite(s[:, 1]).all() and (q[1].float() == 448).all()
 
 
+@pytest.mark.parametrize("M", [9, 1100])
+def test_add_rmsnorm_groups_near_the_scales_floor(M):
+    """Groups whose largest value lies from 1/8 to 8 times 448 * 2^-126, the scale's floor."""
+    D, steps = 8192, 64
+    g = gen(M)
+    x = (torch.randn(M, D, generator=g, device="cuda")
+         * torch.linspace(1, 2, M, device="cuda")[:, None]).bfloat16()  # every factor of the root
+    e = torch.linspace(-3, 3, steps, device="cuda").exp2() * 2.0 ** -118
+    gamma = e.repeat_interleave(128).bfloat16()
+    q, s, _ = dfk.dfk_add_rmsnorm_fp8_block(x, None, gamma, 1e-5)
+    d = x.double()
+    v = d / (d.square().mean(1, keepdim=True) + 1e-5).sqrt() * gamma.double()
+    # as in test_add_rmsnorm, and a few steps 2^-149 where a value is subnormal
+    check_quantised(q, s, v, 2.0 ** -18 * v.abs() + 2.0 ** -147)
+
+
+@pytest.mark.parametrize("M", [3, 1100])
+def test_add_rmsnorm_overflow_is_the_headers_rule(M):
+    """An element whose normalised value passes fp32: infinite scale, its own code NaN, the
+    others 0; the next group is untouched."""
+    x = torch.ones(M, 256, device="cuda", dtype=torch.bfloat16)
+    x[:, 5] = 2                            # 2 / sqrt(259 / 256) * 3.39e38; the ones stay finite
+    gamma = torch.ones(256, device="cuda", dtype=torch.bfloat16)
+    gamma[:128] = torch.finfo(torch.bfloat16).max
+    q, s, _ = dfk.dfk_add_rmsnorm_fp8_block(x, None, gamma, 1e-5)
+    f = q.float()
+    assert torch.isinf(s[0]).all() and torch.isnan(f[:, 5]).all()
+    f[:, 5] = 0
+    assert (f[:, :128] == 0).all()
+    assert torch.isfinite(s[1]).all() and (f[:, 128:] == 448).all()
+
+
 # ---- products
 
 SHAPES = [(1, 16, 1), (1, 128, 128), (2, 144, 130), (1, 4096, 512), (3, 2064, 1001),
