@@ -128,8 +128,10 @@ __device__ __forceinline__ void cluster_sync_all() {
 }
 
 // As cluster_sync_all, ordering nothing: for CTAs that only wait until the others
-// have read their shared memory (every value read has been used by then).  The
-// release of the ordered form waits for the thread's global stores, 0.8 us at
+// have read their shared memory.  A warp comes here with no read outstanding only
+// if something before has used each value it read: the sums below read no column
+// that is not stored, and a store cannot be issued before its operands are there.
+// The release of the ordered form waits for the thread's global stores, 0.8 us at
 // the end of a call.
 __device__ __forceinline__ void cluster_sync_relaxed() {
   __syncwarp();
@@ -159,9 +161,10 @@ __device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr) {
 
 // The cluster's shares of a token's sums (NV values of four columns, `vstep`
 // bytes apart) added in rank order; at: this CTA's address of the first, the
-// same in every CTA.  Four ranks' loads are on their way together.
+// same in every CTA.  Four ranks' loads are on their way together.  Only the first
+// nv values are read, the others are zero (cluster_sync_relaxed).
 template <int NV>
-__device__ __forceinline__ void fb_sum_shares(uint32_t at, uint32_t vstep, int ks,
+__device__ __forceinline__ void fb_sum_shares(uint32_t at, uint32_t vstep, int ks, int nv,
                                               float4 (&sum)[NV]) {
 #pragma unroll
   for (int v = 0; v < NV; ++v) sum[v] = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -171,8 +174,8 @@ __device__ __forceinline__ void fb_sum_shares(uint32_t at, uint32_t vstep, int k
     for (int r = 0; r < 4; ++r)
 #pragma unroll
       for (int v = 0; v < NV; ++v)
-        o[r][v] = r0 + r < ks ? ld_cluster_f4(cluster_map(at + v * vstep, r0 + r))
-                              : make_float4(0.f, 0.f, 0.f, 0.f);
+        o[r][v] = r0 + r < ks && v < nv ? ld_cluster_f4(cluster_map(at + v * vstep, r0 + r))
+                                        : make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
     for (int r = 0; r < 4; ++r)
 #pragma unroll
@@ -256,7 +259,8 @@ __device__ __forceinline__ void fb_emit4_codes(const FbParams &p, int m, int blk
 // rows of block `blk` (one group), summed over the cluster's CTAs in rank order.
 // at: shared-memory address of token 0's 128 gate sums, `tstep` bytes from token to
 // token, `mstep` from a token's gate sums to its up sums.  Eight lanes take a
-// token, sixteen rows each; this warp is the w-th of nw in CTA `rank`.  (A token a
+// token, sixteen rows each; this warp is the w-th of nw in CTA `rank`.  Rows at or
+// past N, which are not stored, are not read (cluster_sync_relaxed).  (A token a
 // turn and warp: 64 tokens took 3 us, each a chain of loads, SiLU, five shuffles,
 // two reciprocals.)
 __device__ __forceinline__ void fb_emit_codes(const FbParams &p, uint32_t at, uint32_t tstep,
@@ -266,6 +270,7 @@ __device__ __forceinline__ void fb_emit_codes(const FbParams &p, uint32_t at, ui
   for (int quad = rank * nw + w; 4 * quad < nt; quad += nw * ks) {
     const int n = 4 * quad + (lane >> 3);
     const uint32_t mine = at + static_cast<uint32_t>(min(n, nt - 1)) * tstep + 16 * l;
+    const int j = blk * 128 + 4 * l;  // and 32 further on for each i; N % 16 == 0
     float h[16], u[16];
 #pragma unroll
     for (int i = 0; i < 16; ++i) h[i] = u[i] = 0.f;
@@ -274,8 +279,11 @@ __device__ __forceinline__ void fb_emit_codes(const FbParams &p, uint32_t at, ui
       float4 g[4], v[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        g[i] = ld_cluster_f4(src + 128 * i);
-        v[i] = ld_cluster_f4(src + 128 * i + mstep);
+        g[i] = v[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (j + 32 * i < p.N) {
+          g[i] = ld_cluster_f4(src + 128 * i);
+          v[i] = ld_cluster_f4(src + 128 * i + mstep);
+        }
       }
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
@@ -289,12 +297,11 @@ __device__ __forceinline__ void fb_emit_codes(const FbParams &p, uint32_t at, ui
         u[4 * i + 3] += v[i].w;
       }
     }
-    const int j = blk * 128 + 4 * l;  // and 32 further on for each i
     float mx = 0.f;
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
       h[i] = fb_silu_mul(h[i], u[i]);
-      if (j + 32 * (i >> 2) < p.N) mx = max_nan(mx, fabsf(h[i]));  // N % 16 == 0
+      mx = max_nan(mx, fabsf(h[i]));
     }
 #pragma unroll
     for (int d = 4; d >= 1; d >>= 1) mx = max_nan(mx, __shfl_xor_sync(0xffffffffu, mx, d));

@@ -652,16 +652,18 @@ __global__ void __launch_bounds__(FBL_THREADS, 1)
       int tm, tn;
       tiles.at(unit, tm, tn);
       const int nt = min(128, p.M - tm * 128);
+      const int nv = GATE || tn * 256 + 128 < p.N ? 2 : 1;  // a second block of 128 columns
       for (int n = kr * 8 + (warp - 4); n < nt; n += 8 * ks) {
         float4 a[2];
-        fb_sum_shares<2>(sbase + static_cast<uint32_t>(n * FBL_PART_ROW + 16 * lane), 512, ks, a);
+        fb_sum_shares<2>(sbase + static_cast<uint32_t>(n * FBL_PART_ROW + 16 * lane), 512, ks, nv,
+                         a);
         const int m = tm * 128 + n;
         if constexpr (GATE) {
           if (p.y == nullptr) fb_emit4_codes(p, m, tn, lane, a[0], a[1]);
           else fb_emit4<2>(p, m, tn, lane, a[0], a[1]);
         } else {
           fb_emit4<1>(p, m, 2 * tn, lane, a[0], a[0]);
-          fb_emit4<1>(p, m, 2 * tn + 1, lane, a[1], a[1]);
+          if (nv == 2) fb_emit4<1>(p, m, 2 * tn + 1, lane, a[1], a[1]);
         }
       }
     }

@@ -333,7 +333,7 @@ __global__ void __launch_bounds__(FbsShape<NMAT, BN>::threads)
       for (int n = rank * Sh::warps + (warp - 2); n < nt; n += Sh::warps * ks) {
         float4 a[NMAT];
         fb_sum_shares<NMAT>(sbase + static_cast<uint32_t>((n * 128 + 4 * lane) * 4), BN * 512, ks,
-                            a);
+                            NMAT, a);
         fb_emit4<NMAT>(p, n0 + n, blk, lane, a[0], a[NMAT - 1]);
       }
     }

@@ -321,6 +321,35 @@ def test_forms_for_many_tokens(M, K, N, op):
         check_rounded(out, ref, err, 2.0 ** -8)
 
 
+# Clusters that add their shares of a part block of columns: two and four CTAs of the tensor-bound
+# kernel with no column in their second 128 (plain), of both kernels with 16 or 48 in the last
+# group (gated).
+@pytest.mark.parametrize("M,K,N,op", [(150, 4112, 6465, "gemm"), (150, 6160, 3905, "gemm"),
+                                      (20, 4096, 688, "fp8"), (40, 4096, 688, "fp8"),
+                                      (130, 8208, 1808, "fp8"), (130, 8208, 1808, "bf16")])
+def test_shared_sums_of_a_part_block(M, K, N, op):
+    g = gen(M + N)
+    q_x, s_x = activations(g, M, K)
+    w = [weights(g, N, K) for _ in range(1 if op == "gemm" else 2)]
+
+    def call():
+        if op == "gemm":
+            return (dfk.dfk_gemm_fp8_block(q_x, s_x, *w[0]),)
+        out = dfk.dfk_swiglu_gate_up_fp8_block(q_x, s_x, *w[0], *w[1], fp8_out=op == "fp8")
+        return out if op == "fp8" else (out,)
+
+    out = call()
+    ref, err = product(q_x, s_x, *w[0])
+    if op != "gemm":
+        ref, err = silu_mul(ref, err, *product(q_x, s_x, *w[1]))
+    if op == "fp8":
+        check_quantised(*out, ref, err)
+    else:
+        check_rounded(out[0], ref, err, 2.0 ** -8)
+    again = [call() for _ in range(50)]      # back to back: the next call's CTAs take over at once
+    assert all(same(out, o) for o in again)
+
+
 def test_codes_as_bytes():
     g = gen(8)
     q_x, s_x = activations(g, 70, 256)
