@@ -52,7 +52,7 @@ constexpr int FBQ_ROWS = 4;
 // rows of 14336 in 14.7 us, 92 % of the copy rate (17.2 us when every lane worked
 // out every row's scale and maximum in fp32: 13 instructions an element).
 __global__ void __launch_bounds__(FBQ_THREADS)
-    fb_quant_kernel(const uint16_t *__restrict__ x, uint8_t *__restrict__ q,
+    fb_quant_kernel(const uint16_t *x, uint8_t *__restrict__ q,
                     float *__restrict__ s, int M, int K, int G, long long items, unsigned *err) {
   const long long item =
       (static_cast<long long>(blockIdx.x) * FBQ_THREADS + threadIdx.x) >> 4;
@@ -69,7 +69,7 @@ __global__ void __launch_bounds__(FBQ_THREADS)
   for (int r = 0; r < FBQ_ROWS; ++r) {
     w[r] = make_uint4(0u, 0u, 0u, 0u);
     if (in && m0 + r < M && DFK_IN_BOUNDS(k + 8 <= K, 20, err))
-      w[r] = ld_nc_v4(x + static_cast<size_t>(m0 + r) * K + k);
+      w[r] = fb_ld_v4(x + static_cast<size_t>(m0 + r) * K + k);
   }
   // Magnitudes stay in bf16 (exact) until the group's is known: two rows share
   // a register in the butterfly over the 16 lanes.

@@ -102,6 +102,22 @@ def test_fast_calls_refuse_quietly(L):
         assert call() is None and call(*[x] * (n + 1)) is None
 
 
+def test_what_the_previous_call_may_write_is_no_read_only_memory():
+    """The read-only path may serve what the memory held before the previous kernel wrote it: only
+    gamma, weights and their scales, which are read early by contract, may take it."""
+    import glob
+    import os
+    import re
+    csrc = os.path.join(os.path.dirname(dfk.__file__), "csrc")
+    loads = []
+    for path in sorted(glob.glob(os.path.join(csrc, "fp8_block*.cu*"))):
+        with open(path) as f:
+            code = re.sub(r"//[^\n]*", "", f.read())
+        assert "ld.global.nc" not in code
+        loads += re.findall(r"(?:__ldg|ld_nc_v4)\(\s*((?:[^();]|\([^();]*\))*)\)", code)
+    assert loads and all(re.search(r"gamma|p\.sw\[", arg) for arg in loads), loads
+
+
 @pytest.mark.parametrize("N,K", [(1, 16), (128, 128), (129, 144), (300, 272)])
 def test_weight_encoder(N, K):
     g = torch.Generator().manual_seed(N)

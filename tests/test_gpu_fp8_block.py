@@ -531,6 +531,46 @@ def test_layer_in_a_graph_and_on_two_streams(M):
     assert all(same(o, l(*x)) for o, l, x in zip(outs, layers, xs))
 
 
+@pytest.mark.parametrize("M", [1, 16, 50, 200])
+def test_a_chain_of_calls_in_the_same_buffers(M):
+    """Every call rewrites what the call before the last one read, a hundred times over."""
+    g = gen(M)
+    n = 512
+    w = [weights(g, n, n) for _ in range(3)]
+    gamma = (1 + 0.1 * torch.randn(n, generator=g, device="cuda")).bfloat16()
+    x0 = rand_bf16(g, M, n)
+
+    def chain(fixed):
+        x, res = x0.clone(), x0.clone()
+        torch.cuda.synchronize()
+        q = s = qh = sh = y = None
+        if fixed:
+            q, qh = (torch.empty(M, n, dtype=E4M3, device="cuda") for _ in range(2))
+            s, sh = (torch.empty(4, M, device="cuda") for _ in range(2))
+            y = x
+        for i in range(100):
+            a = dfk.dfk_add_rmsnorm_fp8_block(x, res, gamma, 1e-5, residual_out=res, q=q, s=s)
+            if not fixed:
+                torch.cuda.synchronize()
+            b = dfk.dfk_swiglu_gate_up_fp8_block(a[0], a[1], *w[0], *w[1], q_h=qh, s_h=sh)
+            if not fixed:
+                torch.cuda.synchronize()
+            x = dfk.dfk_gemm_fp8_block(*b, *w[2], y=y)
+            if not fixed:
+                torch.cuda.synchronize()
+            c = dfk.dfk_quant_fp8_block(x, q=q, s=s)
+            if not fixed:
+                torch.cuda.synchronize()
+            x = dfk.dfk_gemm_fp8_block(*c, *w[2], y=y)
+            if not fixed:
+                torch.cuda.synchronize()
+        return x, res
+
+    want = chain(False)
+    assert torch.isfinite(want[1].float()).all()
+    assert same(chain(True), want)
+
+
 @pytest.mark.parametrize("B", [4, 100])
 def test_decode_stack_in_block_scaled_fp8(B):
     from swiglu_mlp_dfk_b200.stack import DecodeStack
