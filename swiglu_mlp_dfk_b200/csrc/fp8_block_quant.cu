@@ -200,9 +200,23 @@ __global__ void __launch_bounds__(1024)
   for (int i = 1; i < CPT; ++i) mine = li == i ? top[i] : mine;
   const float s_v = fb_group_scale(mine * t);
   float s_u = fb_group_scale(mine);
-  // its sign tells the group's lanes that they divide v, not u, by it
-  if (!(s_u > 1.17549435e-38f && s_v <= 3.402823466e38f)) s_u = -s_v;
-  const float inv = 1.0f / fabsf(s_u);
+  const bool by_v = mine > 0.f && !(s_u > 1.17549435e-38f && s_v <= 3.402823466e38f);
+  if (by_v) s_u = s_v;
+  const float inv = 1.0f / s_u;
+  const unsigned which = __ballot_sync(0xffffffffu, by_v) >> (tid & 16);
+  if (which & 0xffffu) {
+    // A loop that is not unrolled, so that the compiler makes it a branch: as
+    // predicated products in every warp 4096 rows of 8192 take 39.0 us, not 38.6.
+#pragma unroll 1
+    for (int j = 0; j < 8; ++j)
+#pragma unroll
+      for (int i = 0; i < CPT; ++i) {
+        const float next = (which >> i & 1) ? u[i][0] * t : u[i][0];
+#pragma unroll
+        for (int e = 0; e < 7; ++e) u[i][e] = u[i][e + 1];
+        u[i][7] = next;
+      }
+  }
   {
     const int k = 8 * (tid - l + T * li);  // the group's first element
     if (l < CPT && k < D && DFK_IN_BOUNDS(k / FB_GROUP < G && m < M, 26, err))
@@ -211,12 +225,8 @@ __global__ void __launch_bounds__(1024)
 #pragma unroll
   for (int i = 0; i < CPT; ++i) {
     const int k = 8 * (tid + T * i);
-    const float su = __shfl_sync(0xffffffffu, s_u, i, 16);
-    const FbScale f = fb_scale_of(fabsf(su), __shfl_sync(0xffffffffu, inv, i, 16));
-    if (su < 0.f) {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) u[i][j] *= t;
-    }
+    const FbScale f = fb_scale_of(__shfl_sync(0xffffffffu, s_u, i, 16),
+                                  __shfl_sync(0xffffffffu, inv, i, 16));
     if (k < D && DFK_IN_BOUNDS(k + 8 <= D && m < M, 25, err))
       *reinterpret_cast<uint2 *>(q + row + k) =
           make_uint2(fb_codes4(u[i][0], u[i][1], u[i][2], u[i][3], f),
