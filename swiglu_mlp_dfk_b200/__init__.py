@@ -207,6 +207,30 @@ def _stream(stream):
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
+def _torch_stream(stream, device):
+    """A given stream (an object or a handle) as torch's."""
+    if isinstance(stream, torch.cuda.Stream):
+        return stream
+    handle = _stream(stream)
+    return (torch.cuda.ExternalStream(handle, device=device) if handle
+            else torch.cuda.default_stream(device))
+
+
+def _new(stream, device, dtype, *sizes):
+    """An output.  For a given stream it comes from that stream's memory: the current stream's
+    may have been freed with work still queued that writes it.  It is also kept for the current
+    stream, where the caller goes on with it."""
+    if stream is None:
+        return torch.empty(*sizes, dtype=dtype, device=device)
+    own = _torch_stream(stream, device)
+    here = torch.cuda.current_stream(device)
+    with torch.cuda.stream(own):
+        t = torch.empty(*sizes, dtype=dtype, device=device)
+    if t.numel() and here.cuda_stream != own.cuda_stream:
+        t.record_stream(here)
+    return t
+
+
 _BF16 = torch.bfloat16
 
 
@@ -243,7 +267,7 @@ def dfk_swiglu_gate_up(x, w_gate, w_up=None, layout=DFK_W_ROW_MAJOR, h=None, var
         _dev_bf16(n, t)
     B, D, F = _gate_up_shapes(x, w_gate, layout)
     if h is None:
-        h = torch.empty((B, F), dtype=torch.bfloat16, device=x.device)
+        h = _new(stream, x.device, _BF16, B, F)
     _check(lib().dfk_swiglu_gate_up(_ptr(x), _ptr(w_gate), _ptr(w_up), layout, _ptr(h), B, D, F,
                                     int(variant), _stream(stream)))
     return h
@@ -257,7 +281,7 @@ def dfk_rmsnorm_swiglu_gate_up(x, gamma, eps, w_gate, w_up=None, layout=DFK_W_RO
         _dev_bf16(n, t)
     B, D, F = _gate_up_shapes(x, w_gate, layout)
     if h is None:
-        h = torch.empty((B, F), dtype=torch.bfloat16, device=x.device)
+        h = _new(stream, x.device, _BF16, B, F)
     _check(lib().dfk_rmsnorm_swiglu_gate_up(_ptr(x), _ptr(gamma), float(eps), _ptr(w_gate),
                                             _ptr(w_up), layout, _ptr(h), B, D, F, int(variant),
                                             _stream(stream)))
@@ -271,7 +295,7 @@ def dfk_down_proj(h, w_down, y=None, variant=0, stream=None):
     B, F = h.shape
     D = w_down.shape[0]
     if y is None:
-        y = torch.empty((B, D), dtype=torch.bfloat16, device=h.device)
+        y = _new(stream, h.device, _BF16, B, D)
     _check(lib().dfk_down_proj(_ptr(h), _ptr(w_down), _ptr(y), B, D, F, int(variant),
                                _stream(stream)))
     return y
@@ -287,7 +311,7 @@ def dfk_down_proj_static_scratch(h, w_down, y=None, stream=None):
     B, F = h.shape
     D = w_down.shape[0]
     if y is None:
-        y = torch.empty((B, D), dtype=torch.bfloat16, device=h.device)
+        y = _new(stream, h.device, _BF16, B, D)
     _check(lib().dfk_down_proj_static_scratch(_ptr(h), _ptr(w_down), _ptr(y), B, D, F,
                                               _stream(stream)))
     return y
@@ -315,7 +339,7 @@ def dfk_swiglu_gate_up_fp8(x, q_gate, s_gate, q_up, s_up, h=None, variant=0, str
     _dev_fp8(q_gate, s_gate, F)
     _dev_fp8(q_up, s_up, F)
     if h is None:
-        h = torch.empty((B, F), dtype=torch.bfloat16, device=x.device)
+        h = _new(stream, x.device, _BF16, B, F)
     _check(lib().dfk_swiglu_gate_up_fp8(_ptr(x), _ptr(q_gate), _ptr(s_gate), _ptr(q_up),
                                         _ptr(s_up), _ptr(h), B, D, F, int(variant),
                                         _stream(stream)))
@@ -333,7 +357,7 @@ def dfk_rmsnorm_swiglu_gate_up_fp8(x, gamma, eps, q_gate, s_gate, q_up, s_up, h=
     _dev_fp8(q_gate, s_gate, F)
     _dev_fp8(q_up, s_up, F)
     if h is None:
-        h = torch.empty((B, F), dtype=torch.bfloat16, device=x.device)
+        h = _new(stream, x.device, _BF16, B, F)
     _check(lib().dfk_rmsnorm_swiglu_gate_up_fp8(_ptr(x), _ptr(gamma), float(eps), _ptr(q_gate),
                                                 _ptr(s_gate), _ptr(q_up), _ptr(s_up), _ptr(h),
                                                 B, D, F, int(variant), _stream(stream)))
@@ -349,7 +373,7 @@ def dfk_down_proj_fp8(h, q_down, s_down, y=None, variant=0, stream=None):
     D = q_down.shape[0]
     _dev_fp8(q_down, s_down, D)
     if y is None:
-        y = torch.empty((B, D), dtype=torch.bfloat16, device=h.device)
+        y = _new(stream, h.device, _BF16, B, D)
     _check(lib().dfk_down_proj_fp8(_ptr(h), _ptr(q_down), _ptr(s_down), _ptr(y), B, D, F,
                                    int(variant), _stream(stream)))
     return y
@@ -366,7 +390,7 @@ def dfk_rmsnorm_qkv_proj(x, gamma, eps, w_qkv, n_q, n_k, n_v, q=None, k=None, v=
         raise DfkError(DFK_ERR_INVALID_ARG, "w_qkv must be [n_q + n_k + n_v, d_model]")
     outs = []
     for t, n in ((q, n_q), (k, n_k), (v, n_v)):
-        outs.append(torch.empty((B, n), dtype=torch.bfloat16, device=x.device) if t is None else t)
+        outs.append(_new(stream, x.device, _BF16, B, n) if t is None else t)
     _check(lib().dfk_rmsnorm_qkv_proj(_ptr(x), _ptr(gamma), float(eps), _ptr(w_qkv),
                                       _ptr(outs[0]) if n_q else None,
                                       _ptr(outs[1]) if n_k else None,
@@ -473,25 +497,14 @@ def _fb_call(dev, stream, fn, *args):
             _check(fn(*args, _stream(stream)))
 
 
-def _fb_keep(t, stream):
-    """An output allocated here and written on a given stream is kept for that stream."""
-    if t.numel():
-        t.record_stream(stream if hasattr(stream, "cuda_stream")
-                        else torch.cuda.ExternalStream(int(stream), device=t.device))
-
-
 def _fb_codes_out(q, s, M, K, dev, stream, device):
     G = (K + 127) >> 7
     if q is None:
-        q = torch.empty(M, K, dtype=_E4M3, device=device)  # separate sizes: 1 us less
-        if stream is not None:
-            _fb_keep(q, stream)
+        q = _new(stream, device, _E4M3, M, K)
     else:
         _fb_check("q", q, _FP8_CODES, (M, K), dev)
     if s is None:
-        s = torch.empty(G, M, dtype=_F32, device=device)
-        if stream is not None:
-            _fb_keep(s, stream)
+        s = _new(stream, device, _F32, G, M)
     else:
         _fb_check("s", s, _F32_ONLY, (G, M), dev)
     return q, s
@@ -527,9 +540,7 @@ def dfk_add_rmsnorm_fp8_block(x, residual, gamma, eps, residual_out=None, q=None
         _fb_check("residual", residual, _BF16_ONLY, (M, D), dev)
         p_res = residual.data_ptr()
         if residual_out is None:
-            residual_out = torch.empty_like(residual)
-            if stream is not None:
-                _fb_keep(residual_out, stream)
+            residual_out = _new(stream, x.device, _BF16, M, D)
             p_out = residual_out.data_ptr()
     if residual_out is not None and p_out is None:
         _fb_check("residual_out", residual_out, _BF16_ONLY, (M, D), dev)
@@ -552,9 +563,7 @@ def dfk_gemm_fp8_block(q_x, s_x, q_w, s_w, y=None, stream=None):
             return out
     M, K, N, _, dev = _fb_operands(q_x, s_x, q_w, s_w, "q_w")
     if y is None:
-        y = torch.empty(M, N, dtype=_BF16, device=s_x.device)
-        if stream is not None:
-            _fb_keep(y, stream)
+        y = _new(stream, s_x.device, _BF16, M, N)
     else:
         _fb_check("y", y, _BF16_ONLY, (M, N), dev)
     _fb_call(dev, stream, (_lib or lib()).dfk_gemm_fp8_block, q_x.data_ptr(), s_x.data_ptr(),
@@ -584,9 +593,7 @@ def dfk_swiglu_gate_up_fp8_block(q_x, s_x, q_gate, s_gate, q_up, s_up, fp8_out=T
         if q_h is not None or s_h is not None:
             raise DfkError(DFK_ERR_INVALID_ARG, "q_h and s_h are the FP8 output: fp8_out=True")
         if h is None:
-            h = torch.empty(M, F, dtype=_BF16, device=s_x.device)
-            if stream is not None:
-                _fb_keep(h, stream)
+            h = _new(stream, s_x.device, _BF16, M, F)
         else:
             _fb_check("h", h, _BF16_ONLY, (M, F), dev)
         ph = h.data_ptr()
@@ -603,7 +610,7 @@ def dfk_gemv(x, w, out=None, variant=0, stream=None):
     B, K = x.shape
     N = w.shape[0]
     if out is None:
-        out = torch.empty((B, N), dtype=torch.bfloat16, device=x.device)
+        out = _new(stream, x.device, _BF16, B, N)
     _check(lib().dfk_gemv(_ptr(x), _ptr(w), _ptr(out), B, K, N, int(variant), _stream(stream)))
     return out
 
@@ -614,7 +621,7 @@ def dfk_rmsnorm(x, gamma, eps, out=None, stream=None):
         _dev_bf16(n, t)
     B, D = x.shape
     if out is None:
-        out = torch.empty_like(x)
+        out = _new(stream, x.device, _BF16, x.shape)
     _check(lib().dfk_rmsnorm(_ptr(x), _ptr(gamma), float(eps), _ptr(out), B, D, _stream(stream)))
     return out
 
@@ -625,7 +632,7 @@ def dfk_rms_rescale(y, eps=1e-5, out=None, stream=None):
         _dev_bf16(n, t)
     B, D = y.shape
     if out is None:
-        out = torch.empty_like(y)
+        out = _new(stream, y.device, _BF16, y.shape)
     _check(lib().dfk_rms_rescale(_ptr(y), float(eps), _ptr(out), B, D, _stream(stream)))
     return out
 
@@ -634,7 +641,7 @@ def dfk_silu(a, out=None, stream=None):
     """out = SiLU(a) elementwise (unfused-baseline building block)."""
     _dev_bf16("a", a)
     if out is None:
-        out = torch.empty_like(a)
+        out = _new(stream, a.device, _BF16, a.shape)
     _dev_bf16("out", out)
     _check(lib().dfk_silu(_ptr(a), _ptr(out), a.numel(), _stream(stream)))
     return out
@@ -645,7 +652,7 @@ def dfk_mul(a, b, out=None, stream=None):
     _dev_bf16("a", a)
     _dev_bf16("b", b)
     if out is None:
-        out = torch.empty_like(a)
+        out = _new(stream, a.device, _BF16, a.shape)
     _dev_bf16("out", out)
     _check(lib().dfk_mul(_ptr(a), _ptr(b), _ptr(out), a.numel(), _stream(stream)))
     return out
@@ -730,7 +737,9 @@ def dfk_selftest_bounded_wait(elapsed_ns=None, stream=None):
     """Launch the bounded-wait self-test; returns the int64 device tensor that
     receives the time the wait took before giving up (ns)."""
     if elapsed_ns is None:
-        elapsed_ns = torch.zeros(1, dtype=torch.int64, device="cuda")
+        device = torch.device("cuda", torch.cuda.current_device())
+        with torch.cuda.stream(None if stream is None else _torch_stream(stream, device)):
+            elapsed_ns = torch.zeros(1, dtype=torch.int64, device=device)
     _check(lib().dfk_selftest_bounded_wait(_ptr(elapsed_ns), _stream(stream)))
     return elapsed_ns
 
@@ -763,7 +772,7 @@ def dfk_tp_down_proj_allreduce(group, h, w_down_shard, y=None, stream=None):
     B, F = h.shape
     D = w_down_shard.shape[0]
     if y is None:
-        y = torch.empty(B, D, dtype=torch.bfloat16, device=h.device)
+        y = _new(stream, h.device, _BF16, B, D)
     _check(lib().dfk_tp_down_proj_allreduce(group, _ptr(h), _ptr(w_down_shard), _ptr(y), B, D,
                                             F, _stream(stream)))
     return y
@@ -778,7 +787,7 @@ def dfk_tp_down_proj_allreduce_emulated(h_all, w_all, y_all=None, stream=None):
     P, B, F = h_all.shape
     D = w_all.shape[1]
     if y_all is None:
-        y_all = torch.empty(P, B, D, dtype=torch.bfloat16, device=h_all.device)
+        y_all = _new(stream, h_all.device, _BF16, P, B, D)
     _check(lib().dfk_tp_down_proj_allreduce_emulated(P, _ptr(h_all), _ptr(w_all), _ptr(y_all),
                                                      B, D, F, _stream(stream)))
     return y_all
