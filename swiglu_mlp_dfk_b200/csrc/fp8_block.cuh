@@ -81,11 +81,14 @@ __device__ __forceinline__ uint32_t fb_codes4(float v0, float v1, float v2, floa
   return r;
 }
 
-// SiLU(a) * u.  __expf and the approximate division are within a few ulp for
-// |a| < 88 (far inside the 2^-4 step of a code or the 2^-8 of bf16); below
-// -88 the quotient goes to -0, SiLU's limit there.
+// SiLU(a) * u = a e^min(a, 0) / (1 + e^-|a|) * u: the denominator lies in [1, 2],
+// where __fdividef is within 2 ulp.  (a / (1 + e^-a) loses all of SiLU below
+// -87.3, where __fdividef returns 0 for its denominator.)  __expf is within
+// 2 + 1.17 |a| ulp, far inside the 2^-4 step of a code or the 2^-8 of bf16; below
+// -87.3 its result is subnormal, in steps of 2^-149.
 __device__ __forceinline__ float fb_silu_mul(float a, float u) {
-  return __fdividef(a, 1.0f + __expf(-a)) * u;
+  const float e = __expf(-fabsf(a));
+  return __fdividef(a < 0.f ? a * e : a, 1.0f + e) * u;
 }
 
 // Bounded mbarrier wait, as mbar_wait_bounded (same limits, same abort flag and

@@ -379,6 +379,25 @@ def test_silu_far_from_zero():
     assert ((h.double() - ref).abs() <= (2.0 ** -8 + 2.0 ** -12) * ref.abs() + 1e-30).all()
 
 
+@pytest.mark.parametrize("M", [40, 300, 1100])
+def test_silu_of_the_lowest_gates(M):
+    """Gates from -75 to -100, where e^a leaves fp32's normal range, beside a large up."""
+    D, F = 128, 128
+    q_x = torch.zeros(M, D, device="cuda", dtype=E4M3)
+    q_x[:, 0] = 1
+    s_x = torch.linspace(-100, -75, M, device="cuda")[None].contiguous()
+    q_w = torch.ones(F, D, device="cuda").to(E4M3)
+    s_w = torch.ones(1, 1, device="cuda")
+    h = dfk.dfk_swiglu_gate_up_fp8_block(q_x, s_x, q_w, s_w, q_w, s_w * 2.0 ** 100, fp8_out=False)
+    a, u = s_x[0].double(), s_x[0].double() * 2.0 ** 100
+    ref = (a * torch.sigmoid(a) * u)[:, None]
+    # the bound of silu_mul with nothing off before it, one step 2^-149 of the exponential and
+    # half a step of its product with the gate, and bf16's rounding
+    err = ((8 + 2 * a.abs()) * 2.0 ** -23)[:, None] * ref.abs()
+    err = err + (1.5 * a.abs() * 2.0 ** -149 * u.abs())[:, None]
+    check_rounded(h, ref.expand(M, F), err.expand(M, F), 2.0 ** -8)
+
+
 def test_scales_of_every_block_count():
     """One code per group and block: y shows which scale met which."""
     M, K, N = 150, 656, 400
