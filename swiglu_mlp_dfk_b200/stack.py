@@ -58,8 +58,8 @@ class DecodeStack:
     layout: "row", "col", "interleaved" or "auto" -- how the fused bf16
             stack stores W_gate / W_up (converted copies; "auto" asks the
             scheduler); the unfused and FP8 stacks are row-major only
-    fp8:    False, True (codes with row scales) or "block" (block-scaled
-            weights and activations; any number of tokens)
+    fp8:    "block" (block-scaled weights and activations; any number of
+            tokens), otherwise a truth value: codes with row scales or bf16
     """
 
     def __init__(self, layers, x0, eps=1e-5, fused=True, fp8=False, layout="row"):
@@ -71,10 +71,10 @@ class DecodeStack:
             raise ValueError("only the fused bf16 stack takes another weight layout")
         self.eps = float(eps)
         self.fused = fused
-        if fp8 not in (False, True, "block"):
-            raise ValueError("fp8 must be False, True or \"block\"")
+        self.block = isinstance(fp8, str) and fp8 == "block"
+        if isinstance(fp8, str) and fp8 and not self.block:
+            raise ValueError("fp8 must be \"block\" or a truth value")
         self.fp8 = bool(fp8)
-        self.block = fp8 == "block"
         if self.block:
             from . import inputs as I
             layers = [(gamma,) + I.to_fp8_blocks(wg) + I.to_fp8_blocks(wu) + I.to_fp8_blocks(wd)

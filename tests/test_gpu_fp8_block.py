@@ -622,6 +622,17 @@ def test_decode_stack_in_block_scaled_fp8(B):
     assert st.kernels_per_step() == 10 and st.bytes_per_step() > 3 * 3 * 512 * 1040
 
 
+@pytest.mark.parametrize("given,meant", [(None, False), (0, False), (1, True), ("", False)])
+def test_decode_stack_takes_any_truth_value(given, meant):
+    from swiglu_mlp_dfk_b200.stack import DecodeStack
+    x0, params = I.make_stack(1, 2, 256, 272, seed=1, w_std=0.05)
+    a, b = DecodeStack(params, x0, fp8=given), DecodeStack(params, x0, fp8=meant)
+    a.step()
+    b.step()
+    torch.cuda.synchronize()
+    assert torch.equal(a.x, b.x) and a.kernels_per_step() == b.kernels_per_step()
+
+
 def test_large_offsets():
     """Outputs whose offsets pass 32 bits: 70,000 tokens x 32,000 columns of bf16 (4.5 GB)."""
     M, K, N = 70000, 128, 32000
