@@ -15,6 +15,7 @@ profiler-driven scheduler choosing among row-major and column-major kernel
 variants.
 """
 import ctypes
+import importlib.util
 import os
 import threading
 import warnings
@@ -97,7 +98,7 @@ class dfk_variant(ctypes.Structure):
 
 
 _lib = None
-_fast = None  # _dfk_torch.so, bound to the loaded library
+_fast = None  # the module of csrc/torch_calls.cpp, bound to the loaded library
 _lock = threading.Lock()
 
 
@@ -167,18 +168,23 @@ def lib():
 
 
 def _load_calls(L):
-    """Bind csrc/torch_calls.cpp to the library's block-scaled entry points."""
+    """Bind csrc/torch_calls.cpp, as compiled for this torch, to the library's block-scaled
+    entry points."""
     global _fast
+    from . import build
+    path = build.calls_path()
     try:
-        from . import _dfk_torch
+        spec = importlib.util.spec_from_file_location(__name__ + "._dfk_torch", path)
+        calls = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(calls)
     except ImportError as e:
-        warnings.warn("_dfk_torch.so cannot be loaded (%s): calls of the block-scaled FP8 "
-                      "operators take 3-7 us more on the host" % e, RuntimeWarning)
+        warnings.warn("%s cannot be loaded (%s): calls of the block-scaled FP8 operators take "
+                      "3-7 us more on the host" % (path, e), RuntimeWarning)
         return
-    _dfk_torch.bind(*(ctypes.cast(fn, ctypes.c_void_p).value for fn in (
+    calls.bind(*(ctypes.cast(fn, ctypes.c_void_p).value for fn in (
         L.dfk_quant_fp8_block, L.dfk_add_rmsnorm_fp8_block, L.dfk_gemm_fp8_block,
         L.dfk_swiglu_gate_up_fp8_block)))
-    _fast = _dfk_torch
+    _fast = calls
 
 
 def _check(status):

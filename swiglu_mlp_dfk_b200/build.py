@@ -15,13 +15,17 @@ record the first failure in the device status word instead of accessing
 memory) goes to ``_build/checked/`` and ``swiglu_mlp_dfk_b200/libdfk_checked.so``;
 the binding loads it when ``DFK_CHECKED=1`` is set.
 
-``_dfk_torch.so`` (csrc/torch_calls.cpp, g++) holds the host side of the block-scaled
-FP8 calls for the Python binding; libdfk.so does not need it.
+``_dfk_torch-*.so`` (csrc/torch_calls.cpp, g++) holds the host side of the block-scaled
+FP8 calls for the Python binding, for one Python and one torch, which its name
+tells.  Neither libdfk.so nor the binding needs it: where it cannot be built, build()
+warns and the binding makes the calls itself.
 """
 import concurrent.futures as cf
+import contextlib
 import os
 import subprocess
 import sys
+import warnings
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -30,7 +34,6 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libdfk.so")
 LIB_CHECKED = os.path.join(PKG, "libdfk_checked.so")
-LIB_CALLS = os.path.join(PKG, "_dfk_torch.so")
 CALLS_SRC = os.path.join(CSRC, "torch_calls.cpp")
 
 NVCC = os.environ.get("NVCC", "nvcc")
@@ -91,17 +94,20 @@ def _build_one(lib, outdir, extra, force, jobs, verbose):
     return lib
 
 
-def _build_calls(force, verbose):
+def calls_path():
+    """Where csrc/torch_calls.cpp, compiled for this Python and this torch, is kept."""
+    import torch
+    return os.path.join(PKG, "_dfk_torch-%s-torch-%s.so" % (sys.implementation.cache_tag,
+                                                            torch.__version__))
+
+
+def _compile_calls(out):
     """Compile csrc/torch_calls.cpp, a Python module over torch's C++ API, with g++."""
-    header = os.path.join(INCLUDE, "dfk.h")
-    if (not force and os.path.exists(LIB_CALLS)
-            and os.path.getmtime(LIB_CALLS) >= _newest([CALLS_SRC, header])):
-        return
     import sysconfig
 
     import torch
     from torch.utils.cpp_extension import include_paths, library_paths
-    tmp = LIB_CALLS + ".tmp.%d" % os.getpid()
+    tmp = out + ".tmp.%d" % os.getpid()
     cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared",
            "-fvisibility=hidden", "-D_GLIBCXX_USE_CXX11_ABI=%d" % torch._C._GLIBCXX_USE_CXX11_ABI,
            "-I", INCLUDE, "-I", sysconfig.get_paths()["include"]]
@@ -111,16 +117,39 @@ def _build_calls(force, verbose):
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError("g++ failed:\n%s\n%s%s" % (" ".join(cmd), r.stdout, r.stderr))
-    os.replace(tmp, LIB_CALLS)
-    if verbose:
-        print(LIB_CALLS)
+    os.replace(tmp, out)
+
+
+_calls_failed = False  # in this process: not tried again
+
+
+def _build_calls(force, verbose):
+    """Bring the module of calls_path() up to date."""
+    global _calls_failed
+    if _calls_failed and not force:
+        return
+    try:
+        out = calls_path()
+        if (not force and os.path.exists(out) and os.path.getmtime(out) >= _newest(
+                [CALLS_SRC, os.path.join(INCLUDE, "dfk.h")])):
+            return
+        with contextlib.suppress(FileNotFoundError):
+            os.remove(out)         # nothing older than its source is loaded
+        _compile_calls(out)
+        _calls_failed = False
+        if verbose:
+            print(out)
+    except (ImportError, OSError, RuntimeError) as e:
+        _calls_failed = True
+        warnings.warn("%s cannot be built for Python's calls, which take 3-7 us more on the host "
+                      "without it: %s" % (CALLS_SRC, e), RuntimeWarning)
 
 
 def build(force: bool = False, jobs: int = 0, verbose: bool = False,
           checked: bool = True) -> str:
     """Compile every .cu under csrc/ and link libdfk.so (and, with `checked`,
-    the bounds-checked libdfk_checked.so), and _dfk_torch.so; returns the path of
-    libdfk.so."""
+    the bounds-checked libdfk_checked.so), and, where that can be done, the module of
+    calls_path(); returns the path of libdfk.so."""
     lib = _build_one(LIB, BUILD, [], force, jobs, verbose)
     if checked:
         _build_one(LIB_CHECKED, os.path.join(BUILD, "checked"), ["-DDFK_CHECKED"], force, jobs,

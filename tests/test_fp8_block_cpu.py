@@ -118,6 +118,51 @@ def test_what_the_previous_call_may_write_is_no_read_only_memory():
     assert loads and all(re.search(r"gamma|p\.sw\[", arg) for arg in loads), loads
 
 
+@pytest.mark.parametrize("compiler", ["false", "/nonexistent/g++"])
+def test_a_build_without_a_cxx_compiler(monkeypatch, tmp_path, compiler):
+    """The library is built and loaded without the module of the calls."""
+    from swiglu_mlp_dfk_b200 import build
+    monkeypatch.setenv("CXX", compiler)
+    monkeypatch.setattr(build, "PKG", str(tmp_path))
+    monkeypatch.setattr(build, "_calls_failed", False)
+    with pytest.warns(RuntimeWarning, match="cannot be built"):
+        assert build.build() == build.LIB
+    assert not list(tmp_path.iterdir())
+    build.build()                                # not tried, and not said, again
+
+
+def test_a_module_of_the_calls_for_another_torch_is_not_loaded(L, monkeypatch):
+    import os
+
+    from swiglu_mlp_dfk_b200 import build
+    assert dfk._fast is not None and os.path.exists(build.calls_path())
+    monkeypatch.setattr(dfk, "_fast", None)
+    with monkeypatch.context() as m:
+        m.setattr(torch, "__version__", "0.0.0")
+        with pytest.warns(RuntimeWarning, match="cannot be loaded"):
+            dfk._load_calls(L)
+        assert dfk._fast is None
+    dfk._load_calls(L)
+    assert dfk._fast is not None
+
+
+def test_a_module_of_the_calls_older_than_its_source_is_not_kept(monkeypatch, tmp_path):
+    import os
+
+    from swiglu_mlp_dfk_b200 import build
+    monkeypatch.setattr(build, "PKG", str(tmp_path))
+    monkeypatch.setattr(build, "_calls_failed", False)
+    monkeypatch.setenv("CXX", "false")
+    out = build.calls_path()
+    open(out, "wb").close()
+    build._build_calls(False, False)
+    assert os.path.exists(out)                   # newer than its source
+    os.utime(out, (0, 0))
+    with pytest.warns(RuntimeWarning, match="cannot be built"):
+        build._build_calls(False, False)
+    assert not os.path.exists(out)
+
+
 @pytest.mark.parametrize("N,K", [(1, 16), (128, 128), (129, 144), (300, 272)])
 def test_weight_encoder(N, K):
     g = torch.Generator().manual_seed(N)
