@@ -56,7 +56,7 @@ static int ceil_div(long long a, long long b) { return static_cast<int>((a + b -
 // above 16 tokens their meeting costs more than four groups less (24 tokens, d_ff =
 // 1024: K = 4096 8.5 us, 7.8 in clusters of 4; K = 8192 10.4 and 11.0).
 struct SmallPlan {
-  int bn, blocks, tiles, ks;
+  int bn, blocks, tiles, ks, stages;
   bool pack;
   double us;
 };
@@ -74,6 +74,11 @@ static SmallPlan plan_small(const FbCall &c, int G, int sms) {
   if (!s.pack && s.ks == 8 && (work * 8 > sms * 3 / 4 || (s.bn > 16 && G < 64))) s.ks = 4;
   const int waves = ceil_div(work * s.ks, limit);
   s.us = 1.9 + (2.6 + 0.53 * ceil_div(G, s.ks)) * waves;
+  const int cap = s.pack ? FB_SMEM_HALF : FB_SMEM_MAX, most = ceil_div(G, s.ks);
+  s.stages = fb_small_min_stages(c.nmat, s.bn);
+  while (s.stages < 16 && s.stages < most &&
+         fb_small_smem(c.nmat, s.bn, s.stages + 1) <= cap)
+    ++s.stages;
   return s;
 }
 
@@ -99,20 +104,31 @@ static LargePlan plan_large(const FbCall &c, int G, int sms) {
   return best;
 }
 
-// `us` above: what a call takes, fitted to 60 shapes of 48 to 8192 tokens on a
-// B200: a fixed part (launch, first loads; 4 us more where a cluster adds its
-// shares), a part per round of tiles (their output, which the next tile's groups
-// do not hide) and a part per group of a round.  Both sides at 192 tokens:
-// N = 6144, K = 4096 14.0 us streaming, 17.8 by pairs; N = 4096, K = 14336 33.6 us
-// streaming, 23.1 by clusters of 4, 46.5 by pairs; N = 16384, K = 4096 41, 21.5, 20.
-// 8192 tokens, N = 1024, K = 128: 13.6 streaming, 9.4 by pairs, 9.7 by single CTAs.
+// `us` above ranks the forms of one product and tells no more than that (gate/up of
+// 4096 tokens, K = 4096, d_ff = 14336: 342 here, 424 measured in a burst).  It was
+// fitted to calls of 48 to 8192 tokens on a B200: a fixed part (launch, first loads;
+// 4 us more where a cluster adds its shares), a part per round of tiles (their
+// output, which the next tile's groups do not hide) and a part per group of a round.
+// Both sides measured at 192 tokens: N = 6144, K = 4096 14.0 us streaming, 17.8 by
+// pairs; N = 4096, K = 14336 33.6 us streaming, 23.1 by clusters of 4, 46.5 by pairs;
+// N = 16384, K = 4096 41, 21.5, 20.  8192 tokens, N = 1024, K = 128: 13.6 streaming,
+// 9.4 by pairs, 9.7 by single CTAs.
+struct Plan {
+  SmallPlan small;
+  LargePlan large;
+  bool streams;  // the streaming kernel
+};
+
+// Up to 64 tokens the weights' bytes bound every form: the streaming kernel.
+static Plan choose(const FbCall &c, int G, int sms) {
+  Plan p{plan_small(c, G, sms), plan_large(c, G, sms), true};
+  p.streams = c.M <= 64 || p.small.us <= p.large.us;
+  return p;
+}
+
 static int launch_small(const FbCall &c, const SmallPlan &s, int G, unsigned *err,
                         cudaStream_t st) {
   if (s.tiles > 65535) return api_fail(DFK_ERR_UNSUPPORTED_SHAPE, "M=%d is too large", c.M);
-  const int cap = s.pack ? FB_SMEM_HALF : FB_SMEM_MAX;
-  int stages = fb_small_min_stages(c.nmat, s.bn);
-  const int most = ceil_div(G, s.ks);
-  while (stages < 16 && stages < most && fb_small_smem(c.nmat, s.bn, stages + 1) <= cap) ++stages;
   const void *fn = fb_small_kernel(c.nmat, s.bn);
   int rc = api_allow_smem(fn);
   if (rc) return rc;
@@ -122,11 +138,11 @@ static int launch_small(const FbCall &c, const SmallPlan &s, int G, unsigned *er
   for (int m = 0; m < c.nmat; ++m)
     if ((rc = api_tensor_map_u8(c.qw[m], c.K, c.N, c.K, 128, 128, &maps.w[m]))) return rc;
   FbParams p{c.sx, {c.sw[0], c.sw[1]}, static_cast<uint16_t *>(c.y),
-             static_cast<uint8_t *>(c.qh), c.sh, err, c.M, c.N, G, stages, 0};
+             static_cast<uint8_t *>(c.qh), c.sh, err, c.M, c.N, G, s.stages, 0};
   void *args[] = {&maps, &p};
   const cudaError_t e = launch_kernel(
       fn, dim3(static_cast<unsigned>(s.blocks) * s.ks, s.tiles),
-      dim3(fb_small_threads(c.nmat, s.bn)), fb_small_smem(c.nmat, s.bn, stages), st, api_pdl(),
+      dim3(fb_small_threads(c.nmat, s.bn)), fb_small_smem(c.nmat, s.bn, s.stages), st, api_pdl(),
       args, static_cast<unsigned>(s.ks));
   if (e != cudaSuccess) return api_cuda_error(e, "block-scaled FP8 product launch");
   return DFK_OK;
@@ -180,13 +196,10 @@ static int product(const FbCall &c, cudaStream_t st) {
   int sms;
   unsigned *err;
   if ((rc = api_device(&sms, &err))) return rc;
-  // up to 64 tokens the weights' bytes bound every form: the streaming kernel
   const int G = ceil_div(c.K, FB_GROUP);
-  const SmallPlan small = plan_small(c, G, sms);
-  if (c.M <= 64) return launch_small(c, small, G, err, st);
-  const LargePlan large = plan_large(c, G, sms);
-  return small.us <= large.us ? launch_small(c, small, G, err, st)
-                              : launch_large(c, large, G, sms, err, st);
+  const Plan plan = choose(c, G, sms);
+  return plan.streams ? launch_small(c, plan.small, G, err, st)
+                      : launch_large(c, plan.large, G, sms, err, st);
 }
 
 }  // namespace dfk
@@ -247,6 +260,23 @@ int dfk_swiglu_gate_up_fp8_block(const void *q_x, const float *s_x, const void *
                                  void *stream) {
   const FbCall c{2, q_x, s_x, {q_gate, q_up}, {s_gate, s_up}, h, q_h, s_h, M, d_model, d_ff};
   return product(c, static_cast<cudaStream_t>(stream));
+}
+
+// For the tests, which name the forms that they run; not part of dfk.h.  The form of
+// a product with nmat weight matrices on `sms` SMs: {1, tokens of a tile, CTAs of a
+// row block, two CTAs an SM, ring stages} of the streaming kernel, or {0, pairs of
+// CTAs, CTAs of a tile, 0, 0} of the tensor-bound one.
+__attribute__((visibility("default"))) void dfk_fp8_block_form(int nmat, int M, int K, int N,
+                                                               int sms, int form[5]) {
+  FbCall c{};
+  c.nmat = nmat;
+  c.M = M;
+  c.K = K;
+  c.N = N;
+  const Plan p = choose(c, ceil_div(K, FB_GROUP), sms);
+  const int streams[5] = {1, p.small.bn, p.small.ks, p.small.pack, p.small.stages};
+  const int bound[5] = {0, p.large.pair, p.large.pair ? 2 : p.large.ks, 0, 0};
+  memcpy(form, p.streams ? streams : bound, sizeof streams);
 }
 
 }  // extern "C"

@@ -1,12 +1,16 @@
 """Refusals of the block-scaled FP8 operators, checked before any GPU work (fake addresses that
 are never dereferenced), and the weight encoder."""
 import ctypes
+import os
+import sys
 
 import pytest
 import torch
 
 import swiglu_mlp_dfk_b200 as dfk
 from swiglu_mlp_dfk_b200 import inputs as I
+
+sys.path.insert(0, os.path.dirname(os.path.abspath(__file__)))
 
 
 @pytest.fixture(scope="module")
@@ -106,7 +110,6 @@ def test_what_the_previous_call_may_write_is_no_read_only_memory():
     """The read-only path may serve what the memory held before the previous kernel wrote it: only
     gamma, weights and their scales, which are read early by contract, may take it."""
     import glob
-    import os
     import re
     csrc = os.path.join(os.path.dirname(dfk.__file__), "csrc")
     loads = []
@@ -132,8 +135,6 @@ def test_a_build_without_a_cxx_compiler(monkeypatch, tmp_path, compiler):
 
 
 def test_a_module_of_the_calls_for_another_torch_is_not_loaded(L, monkeypatch):
-    import os
-
     from swiglu_mlp_dfk_b200 import build
     assert dfk._fast is not None and os.path.exists(build.calls_path())
     monkeypatch.setattr(dfk, "_fast", None)
@@ -147,8 +148,6 @@ def test_a_module_of_the_calls_for_another_torch_is_not_loaded(L, monkeypatch):
 
 
 def test_a_module_of_the_calls_older_than_its_source_is_not_kept(monkeypatch, tmp_path):
-    import os
-
     from swiglu_mlp_dfk_b200 import build
     monkeypatch.setattr(build, "PKG", str(tmp_path))
     monkeypatch.setattr(build, "_calls_failed", False)
@@ -161,6 +160,25 @@ def test_a_module_of_the_calls_older_than_its_source_is_not_kept(monkeypatch, tm
     with pytest.warns(RuntimeWarning, match="cannot be built"):
         build._build_calls(False, False)
     assert not os.path.exists(out)
+
+
+@pytest.mark.parametrize("nmat", [1, 2])
+def test_the_listed_products_take_every_form(L, nmat):
+    """A change in the choice of form that leaves one without a test fails here."""
+    import math
+    import random
+
+    import fp8_block_forms as forms
+    listed = forms.PLAIN if nmat == 1 else forms.GATED
+    for sizes, form in listed:
+        assert forms.form(nmat, *sizes) == form, sizes
+    rng = random.Random(nmat)
+
+    def spread(lo, hi):
+        return int(math.exp(rng.uniform(math.log(lo), math.log(hi))))
+    met = {forms.form(nmat, spread(1, 5000), 16 * spread(1, 1024), spread(1, 40000))
+           for _ in range(100000)}
+    assert met == {form for _, form in listed}
 
 
 @pytest.mark.parametrize("N,K", [(1, 16), (128, 128), (129, 144), (300, 272)])

@@ -19,6 +19,9 @@ import torch
 import swiglu_mlp_dfk_b200 as dfk
 from swiglu_mlp_dfk_b200 import inputs as I
 
+sys.path.insert(0, os.path.dirname(os.path.abspath(__file__)))
+import fp8_block_forms as forms
+
 pytestmark = pytest.mark.gpu
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 E4M3 = torch.float8_e4m3fn
@@ -348,6 +351,37 @@ def test_shared_sums_of_a_part_block(M, K, N, op):
         check_rounded(out[0], ref, err, 2.0 ** -8)
     again = [call() for _ in range(50)]      # back to back: the next call's CTAs take over at once
     assert all(same(out, o) for o in again)
+
+
+def check_form(op, sizes, form):
+    M, K, N = sizes
+    nmat = 1 if op == "gemm" else 2
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    assert forms.form(nmat, M, K, N, sms) == form
+    g = gen(M + K + N)
+    q_x, s_x = activations(g, M, K)
+    w = [weights(g, N, K) for _ in range(nmat)]
+    ref, err = product(q_x, s_x, *w[0])
+    if op == "gemm":
+        check_rounded(dfk.dfk_gemm_fp8_block(q_x, s_x, *w[0]), ref, err, 2.0 ** -8)
+        return
+    ref, err = silu_mul(ref, err, *product(q_x, s_x, *w[1]))
+    out = dfk.dfk_swiglu_gate_up_fp8_block(q_x, s_x, *w[0], *w[1], fp8_out=op == "fp8")
+    if op == "fp8":
+        check_quantised(*out, ref, err)
+    else:
+        check_rounded(out, ref, err, 2.0 ** -8)
+
+
+@pytest.mark.parametrize("sizes,form", forms.PLAIN)
+def test_gemm_in_every_form(sizes, form):
+    check_form("gemm", sizes, form)
+
+
+@pytest.mark.parametrize("sizes,form", forms.GATED)
+@pytest.mark.parametrize("op", ["fp8", "bf16"])
+def test_gate_up_in_every_form(op, sizes, form):
+    check_form(op, sizes, form)
 
 
 def test_codes_as_bytes():
@@ -880,4 +914,28 @@ def test_checked_build():
     env = dict(os.environ, DFK_CHECKED="1", DFK_ROOT=ROOT)
     r = subprocess.run([sys.executable, "-c", CHILD], env=env, capture_output=True, text=True,
                        timeout=600)
+    assert r.returncode == 0 and "checked ok" in r.stdout, r.stdout + r.stderr
+
+
+CHILD_FORMS = r'''
+import os, sys
+sys.path.insert(0, os.environ["DFK_ROOT"])
+sys.path.insert(0, os.path.join(os.environ["DFK_ROOT"], "tests"))
+import swiglu_mlp_dfk_b200 as dfk
+assert dfk.LIB_PATH.endswith("libdfk_checked.so")
+import test_gpu_fp8_block as t
+for op, listed in (("gemm", t.forms.PLAIN), ("fp8", t.forms.GATED), ("bf16", t.forms.GATED)):
+    for sizes, form in listed:
+        t.check_form(op, sizes, form)
+t.test_add_rmsnorm(1100, 1040, True)
+st = dfk.dfk_device_status()
+assert st[0] == 0, st
+print("checked ok")
+'''
+
+
+def test_checked_build_in_every_form():
+    env = dict(os.environ, DFK_CHECKED="1", DFK_ROOT=ROOT)
+    r = subprocess.run([sys.executable, "-c", CHILD_FORMS], env=env, capture_output=True,
+                       text=True, timeout=600)
     assert r.returncode == 0 and "checked ok" in r.stdout, r.stdout + r.stderr
