@@ -224,7 +224,7 @@ __global__ void __launch_bounds__(CC_MAX_THREADS, 1)
           for (int c = 0; c < 8; ++c) {
             const int k = k0 + 256 * c;
             xv[c] = (k < p.K && DFK_IN_BOUNDS(k + 8 <= p.K, 3, p.err))
-                        ? ld_nc_v4(xr + k) : make_uint4(0u, 0u, 0u, 0u);
+                        ? ld_act_v4(xr + k) : make_uint4(0u, 0u, 0u, 0u);
           }
 #pragma unroll
           for (int c = 0; c < 8; ++c) {
@@ -292,7 +292,7 @@ __global__ void __launch_bounds__(CC_MAX_THREADS, 1)
               const int bb = idx / c8n, k = (idx - bb * c8n) * 8;
               if (b0 + bb < p.B && k < p.K)
                 if (DFK_IN_BOUNDS(b0 + bb < p.B && k + 8 <= p.K, 2, p.err)) {
-                  v[u] = ld_nc_v4(p.x + static_cast<size_t>(b0 + bb) * p.K + k);
+                  v[u] = ld_act_v4(p.x + static_cast<size_t>(b0 + bb) * p.K + k);
                   if (NORM) g[u] = ld_nc_v4(p.gamma + k);
                 }
             }

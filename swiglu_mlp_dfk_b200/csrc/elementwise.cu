@@ -18,7 +18,7 @@ namespace dfk {
 // ascending), then a xor butterfly over the 32 lanes -- so r_b is the same
 // fp32 value.  Unlike the fused prologue (which keeps xn in fp32), this
 // kernel stores xn in HBM and therefore rounds it to bf16.
-__global__ void rmsnorm_rows_kernel(const uint16_t *__restrict__ x,
+__global__ void rmsnorm_rows_kernel(const uint16_t *x,
                                     const uint16_t *__restrict__ gamma, float eps,
                                     uint16_t *__restrict__ out, int B, int D) {
   const int warps = blockDim.x >> 5;
@@ -30,7 +30,7 @@ __global__ void rmsnorm_rows_kernel(const uint16_t *__restrict__ x,
   const uint16_t *xr = x + static_cast<size_t>(row) * D;
   float ss = 0.f;
   for (int k = 8 * lane; k < D; k += 256) {
-    const uint4 v = ld_nc_v4(xr + k);
+    const uint4 v = ld_act_v4(xr + k);
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -43,26 +43,37 @@ __global__ void rmsnorm_rows_kernel(const uint16_t *__restrict__ x,
   for (int m = 16; m >= 1; m >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, m);
   const float r = 1.0f / sqrtf(ss / static_cast<float>(D) + eps);
   uint16_t *orow = out + static_cast<size_t>(row) * D;
-  for (int k = 8 * lane; k < D; k += 256) {
-    const uint4 v = ld_nc_v4(xr + k);
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-    uint32_t g[4] = {0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u};  // 1.0 pairs
-    if (gamma) {
-      const uint4 gv = ld_nc_v4(gamma + k);
-      g[0] = gv.x; g[1] = gv.y; g[2] = gv.z; g[3] = gv.w;
-    }
-    uint32_t o[4];
+  // four chunks' loads before their stores, which no later load may pass
+  for (int k0 = 8 * lane; k0 < D; k0 += 4 * 256) {
+    uint4 xv[4], gv[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const uint32_t lo = f32_to_bf16_bits((bf16_lo(w[i]) * r) * bf16_lo(g[i]));
-      const uint32_t hi = f32_to_bf16_bits((bf16_hi(w[i]) * r) * bf16_hi(g[i]));
-      o[i] = lo | (hi << 16);
+    for (int c = 0; c < 4; ++c) {
+      const int k = k0 + 256 * c;
+      xv[c] = make_uint4(0u, 0u, 0u, 0u);
+      gv[c] = make_uint4(0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u);  // 1.0 pairs
+      if (k < D) {
+        xv[c] = ld_act_v4(xr + k);
+        if (gamma) gv[c] = ld_nc_v4(gamma + k);
+      }
     }
-    *reinterpret_cast<uint4 *>(orow + k) = make_uint4(o[0], o[1], o[2], o[3]);
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      if (k0 + 256 * c >= D) break;
+      const uint32_t w[4] = {xv[c].x, xv[c].y, xv[c].z, xv[c].w};
+      const uint32_t g[4] = {gv[c].x, gv[c].y, gv[c].z, gv[c].w};
+      uint32_t o[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint32_t lo = f32_to_bf16_bits((bf16_lo(w[i]) * r) * bf16_lo(g[i]));
+        const uint32_t hi = f32_to_bf16_bits((bf16_hi(w[i]) * r) * bf16_hi(g[i]));
+        o[i] = lo | (hi << 16);
+      }
+      *reinterpret_cast<uint4 *>(orow + k0 + 256 * c) = make_uint4(o[0], o[1], o[2], o[3]);
+    }
   }
 }
 
-__global__ void silu_kernel(const uint16_t *__restrict__ a, uint16_t *__restrict__ out,
+__global__ void silu_kernel(const uint16_t *a, uint16_t *__restrict__ out,
                             long long n) {
   pdl_wait();
   pdl_launch_dependents();
@@ -73,7 +84,7 @@ __global__ void silu_kernel(const uint16_t *__restrict__ a, uint16_t *__restrict
   }
 }
 
-__global__ void mul_kernel(const uint16_t *__restrict__ a, const uint16_t *__restrict__ b,
+__global__ void mul_kernel(const uint16_t *a, const uint16_t *b,
                            uint16_t *__restrict__ out, long long n) {
   pdl_wait();
   pdl_launch_dependents();
@@ -131,7 +142,7 @@ cudaError_t launch_mul(const void *a, const void *b, void *out, long long n, cud
 // kernel's output (wait before reading); otherwise the loads are issued
 // first and only the stores wait for the previous kernel.
 template <bool WAIT_FIRST>
-__global__ void copy16_kernel(const uint4 *__restrict__ src, uint4 *__restrict__ dst,
+__global__ void copy16_kernel(const uint4 *src, uint4 *__restrict__ dst,
                               size_t n16) {
   if (WAIT_FIRST) pdl_wait();
   pdl_launch_dependents();

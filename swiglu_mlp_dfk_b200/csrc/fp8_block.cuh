@@ -115,22 +115,13 @@ __device__ __forceinline__ bool fb_wait(uint64_t *bar, uint32_t parity, volatile
   }
 }
 
-// What the previous kernel in the stream may write is read by ordinary loads, after
-// pdl_wait.  The read-only path (ld.global.nc, __ldg) is for memory that nothing
-// writes while the reading kernel runs, and under early launch that kernel already
-// runs when the previous one writes; weights, their scales and gamma take it.
+// As ld_act_v4, through L1 (2047 rows of 14336 quantised in 15.6 us, 16.0 without).
 __device__ __forceinline__ uint4 fb_ld_v4(const void *p) {
   uint4 v;
   asm volatile("ld.global.v4.u32 {%0, %1, %2, %3}, [%4];"
                : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
                : "l"(p)
                : "memory");
-  return v;
-}
-
-__device__ __forceinline__ float fb_ld_f32(const float *p) {
-  float v;
-  asm volatile("ld.global.f32 %0, [%1];" : "=f"(v) : "l"(p) : "memory");
   return v;
 }
 

@@ -222,7 +222,7 @@ __global__ void __launch_bounds__(FbsShape<NMAT, BN>::threads)
         const int n = n0 + t0 + lane + 32 * e;
         sx[e] = 0.f;
         if (i < nkb && lane + 32 * e < TN && n < p.M && DFK_IN_BOUNDS(kb < p.G, 27, p.err))
-          sx[e] = fb_ld_f32(p.sx + static_cast<size_t>(kb) * p.M + n);
+          sx[e] = ld_act_f32(p.sx + static_cast<size_t>(kb) * p.M + n);
       }
     };
 #pragma unroll

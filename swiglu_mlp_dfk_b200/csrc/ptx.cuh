@@ -198,6 +198,24 @@ __device__ __forceinline__ void named_barrier(int id, int nthreads) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(nthreads) : "memory");
 }
 
+// What the previous kernel in the stream may write is read by ordinary loads, after
+// pdl_wait.  The read-only path (ld.global.nc, __ldg) is for memory that nothing
+// writes while the reading kernel runs, and under early launch that kernel already
+// runs when the previous one writes; weights, their scales and gamma take it.
+__device__ __forceinline__ uint4 ld_act_v4(const void *p) {
+  uint4 v;
+  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p));
+  return v;
+}
+
+__device__ __forceinline__ float ld_act_f32(const float *p) {
+  float v;
+  asm volatile("ld.global.f32 %0, [%1];" : "=f"(v) : "l"(p));
+  return v;
+}
+
 // Read-only 16-byte global load that bypasses L1 allocation.
 __device__ __forceinline__ uint4 ld_nc_v4(const void *p) {
   uint4 v;

@@ -686,7 +686,7 @@ __global__ void __launch_bounds__(TC_PREP_THREADS, 3) tc_norm_prep_kernel(const 
       const int c = c0 + i * TC_PREP_THREADS;
       xv[i] = gv[i] = make_uint4(0u, 0u, 0u, 0u);
       if (real && c < kchunks && DFK_IN_BOUNDS(8 * c + 8 <= p.K, 7, p.err)) {
-        xv[i] = ld_nc_v4(p.x + static_cast<size_t>(b) * p.K + 8 * c);
+        xv[i] = ld_act_v4(p.x + static_cast<size_t>(b) * p.K + 8 * c);
         gv[i] = ld_nc_v4(p.gamma + 8 * c);
       }
     }

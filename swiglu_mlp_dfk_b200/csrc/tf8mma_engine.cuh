@@ -137,7 +137,7 @@ __device__ __forceinline__ void tm8_load_chunk(const Tm8PrepParams &p, int b, in
                                                uint4 &gv) {
   xv = gv = make_uint4(0u, 0u, 0u, 0u);
   if (!DFK_IN_BOUNDS(b < p.B && 8 * c + 8 <= p.K, 13, p.err)) return;
-  xv = ld_nc_v4(p.x + static_cast<size_t>(b) * p.K + 8 * c);
+  xv = ld_act_v4(p.x + static_cast<size_t>(b) * p.K + 8 * c);
   gv = p.gamma ? ld_nc_v4(p.gamma + 8 * c) : make_uint4(0u, 0u, 0u, 0u);
 }
 
@@ -526,28 +526,31 @@ __global__ void __launch_bounds__(IBP > 0 ? TM8_INK_THREADS : TM8_THREADS, 1)
             else u[e] = acc[e];
           }
         }
+        // the tokens' factors, all loaded before the first store
+        const float *fac = INK ? nullptr
+                               : p.fac + (p.kslices > 1 ? static_cast<size_t>(slc) * p.bnp : 0);
+        float f[16];
+#pragma unroll
+        for (int e = 0; e < 16; ++e)
+          f[e] = e >= cstep ? 0.f : INK ? s_fac[c + e] : ld_act_f32(fac + c + e);
         if (p.kslices > 1) {
           // in-kernel terms: each slice's partial sums at their true scale
           // (times the slice's 2^-e_b; exact)
           float *mine = p.part + (static_cast<size_t>(slc) * p.nblocks + blk) * p.bnp * 128;
 #pragma unroll
           for (int e = 0; e < 16; ++e)
-            if (e < cstep)
-              mine[(c + e) * 128 + row] =
-                  g[e] * (INK ? s_fac[c + e]
-                              : __ldg(p.fac + static_cast<size_t>(slc) * p.bnp + c + e));
+            if (e < cstep) mine[(c + e) * 128 + row] = g[e] * f[e];
         } else if (row < r) {
 #pragma unroll
           for (int e = 0; e < 16; ++e) {
             const int n = c + e;
             if (e < cstep && n < p.B) {
-              const float f = INK ? s_fac[n] : __ldg(p.fac + n);
               float res;
               if (NMAT == 2) {
-                const float a = (g[e] * f) * sg, uu = (u[e] * f) * su;
+                const float a = (g[e] * f[e]) * sg, uu = (u[e] * f[e]) * su;
                 res = (a / (1.0f + expf(-a))) * uu;
               } else {
-                res = (g[e] * f) * sg;
+                res = (g[e] * f[e]) * sg;
               }
               if (DFK_IN_BOUNDS(j < p.N, 11, p.err))
                 p.out[static_cast<size_t>(n) * p.N + j] = f32_to_bf16_bits(res);
@@ -599,7 +602,7 @@ __global__ void __launch_bounds__(IBP > 0 ? TM8_INK_THREADS : TM8_THREADS, 1)
     auto load = [&](int c, uint4 &xv, uint4 &gv) {
       xv = gv = make_uint4(0u, 0u, 0u, 0u);
       if (real && c < c_k) {
-        xv = ld_nc_v4(xr + 8 * c);
+        xv = ld_act_v4(xr + 8 * c);
         if (p.gamma) gv = ld_nc_v4(p.gamma + 8 * c);
       }
     };

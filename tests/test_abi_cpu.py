@@ -265,3 +265,20 @@ int main(void) {
     r = subprocess.run([str(exe)], capture_output=True, text=True, timeout=120)
     assert r.returncode == 0, r.stdout + r.stderr
     assert r.stdout.split()[0] == str(dfk.DFK_ERR_INVALID_ARG)
+
+
+def test_activations_are_no_read_only_memory():
+    """A kernel launched early already runs when the previous one writes its activations: the
+    read-only path (ld.global.nc, const __restrict__ pointers) is left to gamma, weights and
+    their scales, which are read early by contract."""
+    import glob
+    csrc = os.path.join(ROOT, "swiglu_mlp_dfk_b200", "csrc")
+    loads, pointers = [], []
+    for path in sorted(glob.glob(os.path.join(csrc, "*.cu*"))):
+        with open(path) as f:
+            code = re.sub(r"//[^\n]*", "", f.read())
+        loads += re.findall(r"(?:__ldg|ld_nc_v4)\(\s*((?:[^();]|\([^();]*\))*)\)", code)
+        pointers += re.findall(r"const \w+ \*\s*__restrict__ (\w+)", code)
+    loads.remove("const void *p")                # the definition of ld_nc_v4
+    assert loads and all(re.search(r"gamma|p\.sw\[|p\.scale\[", a) for a in loads), loads
+    assert set(pointers) <= {"gamma"}, pointers
