@@ -24,11 +24,13 @@
 // another.  Two warps of their own work out s_x s_w and report through the same
 // barrier as the MMA.
 //
-// Measured (B200): 4096 tokens, K = 4096, gated, d_ff = 14336: 424 us in a burst
+// Measured (B200): 4096 tokens, K = 4096, gated, d_ff = 14336: 425 us in a burst
 // (2.27 PFLOP/s), 490 us for seconds on end (1.97, SM clock 1.4 GHz under the
-// 1000 W limit); K = 14336, N = 4096: 214 and 254 us.  SiLU, the group maximum and
-// the codes of a tile take 5 % of it.  On the way: one barrier per
-// group instead of per half 524 us; loads of 32 TMEM columns instead of 16 680
+// 1000 W limit); K = 14336, N = 4096: 214 and 254 us.  Stamps of the SM clock, which
+// stands at 1.5 GHz from the first of such calls on: 650 to 670 cycles a group, of
+// which the MMA needs 512, and 4400 cycles for a gated tile's output (3900 plain):
+// 17 % of the gated call (25 tiles of 32 groups a pair), 5 % of the plain one (4 of
+// 112).  On the way: one barrier per group instead of per half 524 us; loads of 32 TMEM columns instead of 16 680
 // cycles a group in place of 480 (the allocator copies registers); sixteen epilogue
 // warps of 64 sums no faster; single CTAs in place of pairs 14 % slower.
 #include <algorithm>
