@@ -30,9 +30,10 @@
 // stands at 1.5 GHz from the first of such calls on: 650 to 670 cycles a group, of
 // which the MMA needs 512, and 4400 cycles for a gated tile's output (3900 plain):
 // 17 % of the gated call (25 tiles of 32 groups a pair), 5 % of the plain one (4 of
-// 112).  On the way: one barrier per group instead of per half 524 us; loads of 32 TMEM columns instead of 16 680
-// cycles a group in place of 480 (the allocator copies registers); sixteen epilogue
-// warps of 64 sums no faster; single CTAs in place of pairs 14 % slower.
+// 112).  On the way: one barrier per group instead of per half 524 us; loads of 32
+// TMEM columns instead of 16 680 cycles a group in place of 480 in a test of the loop
+// alone (the allocator copies registers); sixteen epilogue warps of 64 sums no faster;
+// single CTAs in place of pairs 14 % slower.
 #include <algorithm>
 
 #include "fp8_block.cuh"

@@ -49,7 +49,7 @@ constexpr int FBQ_ROWS = 4;
 
 // Half a warp takes one group of 128 of FBQ_ROWS consecutive rows: 16 bytes a
 // lane and row, every load issued before the first use.  Bound by memory: 2047
-// rows of 14336 in 14.7 us, 92 % of the copy rate (17.2 us when every lane worked
+// rows of 14336 in 14.9 us, 91 % of the copy rate (17.2 us when every lane worked
 // out every row's scale and maximum in fp32: 13 instructions an element).
 __global__ void __launch_bounds__(FBQ_THREADS)
     fb_quant_kernel(const uint16_t *x, uint8_t *__restrict__ q,
